@@ -77,7 +77,8 @@ typedef enum {
   MOVA_BF16 = 1,
   MOVA_F16 = 2,
   MOVA_I32 = 3,
-  MOVA_I8 = 4
+  MOVA_I8 = 4,
+  MOVA_E4M3 = 5               /* 8-bit cache pages only (4 exponent, 3 fraction bits, largest 448) */
 } mova_dtype;
 
 /* Which expert kernel runs.  AUTO picks the weight-streaming kernel for
@@ -431,6 +432,144 @@ mova_status mova_value_routed_noalloc(const void* x, mova_dtype x_dt, const floa
                                       const float* br, const void* Wv, mova_dtype wv_dt,
                                       int T, int d, int E, int k, int n, float scale, void* v,
                                       void* stream);
+
+/* ---- Paged key-value cache ---------------------------------------------------
+ *
+ * The value path returns "exactly the tensor a GQA cache holds"; these calls
+ * are that cache and its readers.  Keys and values lie in pages of
+ * page_size tokens; a request's tokens fill the pages that its row of a page
+ * table names, in order, and token i of request b lies at
+ * page table[b, i / page_size], place i % page_size.  A slot is
+ * page * page_size + place.  One serving step is
+ *
+ *   mova_page_map     request lengths -> new pages in the table, a slot and a
+ *                     position for every new token
+ *   (the caller's projections: q, k; v by mova_value_routed)
+ *   mova_page_write   the step's k and v -> their slots
+ *   mova_page_bounds  (sparse attention only) per-page key bounds
+ *   mova_page_attend  one new token per request over its pages; or
+ *   mova_page_select  + mova_page_attend over the pages it picks
+ *
+ * Conventions beyond those at the top of this file:
+ *  - 128 elements per head, as everywhere in this library; query head h reads
+ *    KV head h / G, G = H / kv_heads from 1 to 16.
+ *  - page_size is 16, 32, 64, 128 or 256; at most 4096 requests per call;
+ *    num_pages * page_size < 2^31; max_pages * page_size <= 2^30; requests *
+ *    max_pages * page_size * kv_heads < 2^34.
+ *  - Types: fp32 pages with fp32 q, k, v and outputs; bf16 pages, or E4M3
+ *    pages with one fp32 scale per KV head (value = stored * scale), with
+ *    bf16 q, k, v and outputs.  Other pairs: MOVA_ERR_UNSUPPORTED.
+ *  - A table row has max_pages entries, table_stride entries apart (0:
+ *    max_pages).  Entries past a request's last page are not read.
+ *  - `ws` is device memory, 256-byte aligned: mova_page_workspace_size()
+ *    bytes for mova_page_select and mova_page_attend, 256 for the others.
+ *    Its content need not survive between calls.  Calls on one stream may
+ *    share it; calls that may overlap must not.
+ *  - What only the device can see is checked there: every call writes the
+ *    status word of `ws` (MOVA_OK or MOVA_ERR_DEVICE_CHECK with the index of
+ *    the first offending request, or token for mova_page_write).  Nothing is
+ *    read or written through a bad page or slot: it counts as absent.
+ *  - Requests of length 0 (a padded batch) are valid everywhere.
+ *  - Results do not depend on timing: no atomics order a sum. */
+typedef struct mova_pages {
+  void* k;                  /* (num_pages, kv_heads, page_size, 128) */
+  void* v;                  /* as k; NULL where a call reads only keys */
+  mova_dtype dtype;         /* MOVA_F32, MOVA_BF16 or MOVA_E4M3 */
+  int num_pages;
+  int kv_heads;
+  int page_size;
+  long long k_page_stride;  /* elements from one page to the next (0: dense) */
+  long long v_page_stride;
+  const float* k_scale;     /* MOVA_E4M3: (kv_heads) each, > 0; NULL: 1 */
+  const float* v_scale;
+} mova_pages;
+
+/* Workspace that serves every paged call of these sizes (H query heads).  0
+ * for sizes the calls refuse. */
+size_t mova_page_workspace_size(int B, int max_pages, int kv_heads, int H);
+
+/* Page tables and slot maps of one step, on the device.
+ *   cached, added (B)  int32 tokens of each request before the step, and new
+ *                      in it
+ *   table              int32, the first ceil(cached / page_size) entries of
+ *                      each row given; the entries of new pages are written
+ *   free_pages         (n_free) int32 page numbers to hand out, in order
+ *   taken (1)          int32: how many of them are handed out already
+ *   lens (B)           int32 out: cached + added
+ *   starts (B+1)       int32 out: first new token of each request (an
+ *                      exclusive prefix sum of added)
+ *   slots (T)          int32 out: slot of each new token, -1 past the last
+ *   positions (T)      int32 out: its place in its request, -1 past the last
+ *   taken_out (1)      int32 out, may be `taken`
+ * Request b needs ceil(lens / page_size) - ceil(cached / page_size) new pages
+ * and takes them in request order.  A request is refused when its counts are
+ * negative, it would outgrow its row, or the free pages run out before its
+ * last one: it takes no page, lens[b] = cached[b] (0 if negative), its tokens
+ * get slot and position -1.  A token whose page number lies outside
+ * [0, num_pages) gets slot -1; tokens past T get none.  The status tells the
+ * first request that any of these befell.  `taken` outside [0, n_free] counts
+ * as no page left.  No output may overlap an input, taken_out apart. */
+mova_status mova_page_map(const int32_t* cached, const int32_t* added, int B, int32_t* table, long long table_stride,
+                          int max_pages, const int32_t* free_pages, int n_free, const int32_t* taken, int page_size,
+                          int num_pages, int T, int32_t* lens, int32_t* starts, int32_t* slots, int32_t* positions,
+                          int32_t* taken_out, void* ws, size_t ws_bytes, void* stream);
+
+/* Writes the keys and values of T tokens into their slots.
+ *   k, v   (T, kv_heads, 128) of dtype dt, tokens k_stride / v_stride
+ *          elements apart (0: kv_heads * 128); v is what mova_value_routed
+ *          returns
+ *   slots  (T) int32; -1: the token is not written.  No slot twice: of two
+ *          tokens with one slot, either may be kept, in whole or in parts.
+ * E4M3 pages receive k / k_scale rounded to nearest even and clamped to
+ * +-448 (NaN stays NaN).  A slot outside [-1, num_pages * page_size) is
+ * skipped and reported. */
+mova_status mova_page_write(const void* k, const void* v, mova_dtype dt, long long k_stride, long long v_stride,
+                            const int32_t* slots, int T, const mova_pages* pages, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Per-page key bounds, for mova_page_select: k_lo, k_hi (num_pages, kv_heads,
+ * 128), of the pages' dtype, receive the least and the greatest stored key of
+ * every page that the step filled, in each dimension (NaN if any key there is
+ * NaN): the pages j of request b with cached[b] < (j + 1) * page_size <=
+ * lens[b].  Other pages' bounds stay as they are.  With cached = 0, all full
+ * pages. */
+mova_status mova_page_bounds(const mova_pages* pages, const int32_t* table, long long table_stride, int max_pages,
+                             const int32_t* cached, const int32_t* lens, int B, void* k_lo, void* k_hi, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* Attention of one new token per request over its cached tokens (the new one
+ * included, once written):
+ *   o[b, h] = sum_i p_i v_i / sum_i p_i,  p_i = exp(scale * q[b, h] . k_i),
+ * i over the lens[b] tokens of request b, KV head h / G.
+ *   q    (B, H, 128) of dtype q_dt, requests q_stride elements apart (0: H * 128)
+ *   o    (B, H, 128) dense, of dtype q_dt; zeros where there is no token
+ *   lse  (B, H) fp32, nullable: log of the sum; -inf where there is no token
+ * picked (B, kv_heads, top) int32, nullable (top = 0): only tokens of these
+ * pages (numbers j within the request's row) count, for each KV head its own.
+ * Of each list the first min(top, pages of the request) entries are read;
+ * one that is no page of the request (-1) is skipped; one given twice counts
+ * twice.  Lengths are clamped to [0, max_pages * page_size] and reported. */
+mova_status mova_page_attend(const void* q, mova_dtype q_dt, long long q_stride, int H, const mova_pages* pages,
+                             const int32_t* table, long long table_stride, int max_pages, const int32_t* lens, int B,
+                             float scale, const int32_t* picked, int top, void* o, float* lse, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* The pages worth reading: for each request and KV head, `top` of the
+ * request's pages (all, where it has no more), as page numbers within its row
+ * in ascending order, then -1.  The last page is always among them; of the
+ * others (all full), those with the greatest
+ *   max over the group's heads h of
+ *     sum_d q[b, h, d] * (q[b, h, d] < 0 ? k_lo[d] : k_hi[d]),
+ * which bounds every key's product with q from above.  Formed in fp64, so that
+ * the order of the sum decides no page; equal scores: the lower page number.
+ * A NaN score counts as the greatest.  Scores are of the stored values
+ * (E4M3: without the head's scale, which changes no order).  q as in
+ * mova_page_attend; of `pages` only dtype, num_pages, kv_heads and page_size
+ * are read.  picked (B, kv_heads, top) int32 out. */
+mova_status mova_page_select(const void* q, mova_dtype q_dt, long long q_stride, int H, const mova_pages* pages,
+                             const void* k_lo, const void* k_hi, const int32_t* table, long long table_stride,
+                             int max_pages, const int32_t* lens, int B, int top, int32_t* picked, void* ws,
+                             size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,7 +17,7 @@ STATUS_NAMES = {OK: "MOVA_OK", ERR_INVALID_ARG: "MOVA_ERR_INVALID_ARG",
                 ERR_UNSUPPORTED: "MOVA_ERR_UNSUPPORTED", ERR_CUDA: "MOVA_ERR_CUDA",
                 ERR_TIMEOUT: "MOVA_ERR_TIMEOUT", ERR_DEVICE_CHECK: "MOVA_ERR_DEVICE_CHECK"}
 # mova_dtype
-F32, BF16, F16, I32, I8 = range(5)
+F32, BF16, F16, I32, I8, E4M3 = range(6)
 # mova_path
 PATH_AUTO, PATH_STREAM, PATH_TENSOR, PATH_TENSOR_1CTA = range(4)
 # parts of the workspace (mova_workspace_parts)
@@ -30,6 +30,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 
 class Options(ctypes.Structure):
@@ -37,6 +38,14 @@ class Options(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int), ("events", ctypes.c_void_p),
                 ("wv_expert_stride", ctypes.c_longlong), ("router_partitions", ctypes.c_int),
                 ("decode_launches", ctypes.c_int), ("router_planes", ctypes.c_void_p)]
+
+
+class Pages(ctypes.Structure):
+    """mova_pages (include/mova.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("kv_heads", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("k_page_stride", ctypes.c_longlong), ("v_page_stride", ctypes.c_longlong),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 SIGNATURES = {
@@ -75,6 +84,14 @@ SIGNATURES = {
                              _vp, _vp]),
     "mova_value_routed_opts": (_i, [_vp, _i, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _vp,
                                     _vp, _vp, _sz, _vp, _vp]),
+    "mova_page_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "mova_page_map": (_i, [_vp, _vp, _i, _vp, _ll, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp,
+                           _vp, _sz, _vp]),
+    "mova_page_write": (_i, [_vp, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp, _sz, _vp]),
+    "mova_page_bounds": (_i, [_vp, _vp, _ll, _i, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "mova_page_attend": (_i, [_vp, _i, _ll, _i, _vp, _vp, _ll, _i, _vp, _i, _f, _vp, _i, _vp, _vp, _vp, _sz,
+                              _vp]),
+    "mova_page_select": (_i, [_vp, _i, _ll, _i, _vp, _vp, _vp, _vp, _ll, _i, _vp, _i, _i, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None

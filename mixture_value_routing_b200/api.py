@@ -5,6 +5,12 @@ torch CUDA tensors (torch only provides device memory and the stream).
     idx, w = route(x, Wr, br)
     v = value(x, idx, w, Wv)                    # routing given (compact cache)
 
+and, for the paged key-value cache that v goes into,
+
+    lens, starts, slots, positions, taken = page_map(cached, added, table, free_pages, taken, 64, num_pages, T)
+    page_write(k, v, slots, k_cache, v_cache)
+    o = page_attend(q, k_cache, v_cache, table, lens)
+
 Every function enqueues on torch's current CUDA stream (the host-buffer forms:
 on `stream` if given) and returns without synchronising.  Device-side checks
 are read with get_status().  A call given no `ws` uses the workspace this
@@ -22,7 +28,7 @@ import torch
 from . import _lib
 
 _DT = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16,
-       torch.int32: _lib.I32, torch.int8: _lib.I8}
+       torch.int32: _lib.I32, torch.int8: _lib.I8, torch.float8_e4m3fn: _lib.E4M3}
 _PATH = {"auto": _lib.PATH_AUTO, "stream": _lib.PATH_STREAM, "tensor": _lib.PATH_TENSOR,
          "tensor_1cta": _lib.PATH_TENSOR_1CTA}
 
@@ -452,6 +458,264 @@ def value_attend_host(x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, Wv: t
         _ptr(x), _ptr(idx), _DT[idx.dtype], _ptr(w), _DT[w.dtype], _ptr(Wv), L, d, E, k, n, _ptr(probs), H,
         _ptr(o), _ptr(ws), ws.numel(), _stream(stream)), "mova_value_attend_host")
     return o
+
+
+# ---- Paged key-value cache ------------------------------------------------------
+# Caches are (num_pages, KV heads, page_size, 128) tensors whose pages may lie
+# further apart than dense (a part of a larger tensor); tables (requests,
+# max_pages) int32, rows possibly a part of longer ones; q, k and v rows of a
+# fused projection's output.  Types: fp32 with fp32 caches; bf16 with bf16 or
+# float8_e4m3fn caches, the latter with one fp32 scale per KV head.
+
+_CACHE_IO = {torch.float32: torch.float32, torch.bfloat16: torch.bfloat16, torch.float8_e4m3fn: torch.bfloat16}
+_STATUS_BYTES = 256
+
+
+def _on(dev: torch.device, **tensors) -> None:
+    """Every tensor on `dev`: the library sees addresses only."""
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _elsewhere(t: torch.Tensor) -> bool:
+    """Whether t's device is not the current one (whose stream a call uses)."""
+    if not t.is_cuda:
+        raise ValueError("the paged calls take CUDA tensors")
+    return t.device.index != torch.cuda.current_device()
+
+
+def _vector(t: torch.Tensor, name: str, n: int, dtype=torch.int32) -> None:
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} vector of {n}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _row_stride(t: torch.Tensor, name: str, width: int) -> int:
+    """Elements from one row to the next of a tensor whose rows (all dims but
+    the first) hold `width` elements in order."""
+    want = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != want:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        want *= size
+    if want != width:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected rows of {width} elements")
+    if t.shape[0] <= 1:
+        return width
+    if t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap")
+    return t.stride(0)
+
+
+def _heads(t: torch.Tensor, name: str, dtype) -> None:
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[2] != 128:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (rows, heads, 128)")
+
+
+def _pages(dev, k_cache, v_cache=None, k_scale=None, v_scale=None):
+    """The mova_pages of a cache, and its shape (num_pages, KV heads, page_size)."""
+    dtype, strides = k_cache.dtype, [0, 0]
+    if dtype not in _CACHE_IO:
+        raise ValueError(f"k_cache: dtype {dtype} not in {tuple(_CACHE_IO)}")
+    if k_cache.dim() != 4 or k_cache.shape[3] != 128:
+        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)}, expected (num_pages, KV heads, page_size, 128)")
+    num, kv, page, _ = k_cache.shape
+    for i, (name, t) in enumerate((("k_cache", k_cache), ("v_cache", v_cache))):
+        if t is None:
+            continue
+        if t.dtype != dtype or t.shape != k_cache.shape:
+            raise ValueError(f"{name}: expected {dtype} of shape {tuple(k_cache.shape)}")
+        strides[i] = _row_stride(t, name, kv * page * 128)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None:
+            if dtype != torch.float8_e4m3fn:
+                raise ValueError(f"{name}: only float8_e4m3fn caches have scales")
+            _vector(t, name, kv, torch.float32)
+    _on(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    p = _lib.Pages(k_cache.data_ptr(), 0 if v_cache is None else v_cache.data_ptr(), _DT[dtype], num, kv, page,
+                   strides[0], strides[1], 0 if k_scale is None else k_scale.data_ptr(),
+                   0 if v_scale is None else v_scale.data_ptr())
+    return p, num, kv, page
+
+
+def _table(dev, table, lens, B: int):
+    """(row stride, max_pages) of a page table for B requests."""
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"table: expected int32 of shape ({B}, max_pages), got {table.dtype} {tuple(table.shape)}")
+    _vector(lens, "lens", B)
+    _on(dev, table=table, lens=lens)
+    return _row_stride(table, "table", table.shape[1]), table.shape[1]
+
+
+def _page_ws(ws, nbytes: int, dev):
+    if ws is None:
+        ws = _workspace(nbytes, dev)
+    else:
+        _on(dev, ws=ws)
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+@functools.lru_cache(maxsize=256)
+def page_workspace_size(B: int, max_pages: int, kv_heads: int, H: int) -> int:
+    """Device workspace of every paged call of these sizes (0: refused)."""
+    return int(_lib.load().mova_page_workspace_size(B, max_pages, kv_heads, H))
+
+
+def page_map(cached: torch.Tensor, added: torch.Tensor, table: torch.Tensor, free_pages: torch.Tensor,
+             taken: torch.Tensor, page_size: int, num_pages: int, tokens: int,
+             taken_out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """One step's pages and slots from request lengths (mova_page_map):
+    (lens (B), starts (B+1), slots (tokens), positions (tokens), taken (1)),
+    all int32.  Writes the new pages into `table`; `taken` counts the entries
+    of free_pages handed out so far, and the new count goes to taken_out
+    (which may be `taken` itself) or to a new tensor.  `tokens` is the size of
+    the step's token batch; slots and positions past the last token are -1."""
+    if _elsewhere(cached):
+        with torch.cuda.device(cached.device):
+            return page_map(cached, added, table, free_pages, taken, page_size, num_pages, tokens, taken_out, ws)
+    dev, B = cached.device, cached.shape[0]
+    _vector(cached, "cached", B)
+    _vector(added, "added", B)
+    _vector(free_pages, "free_pages", free_pages.shape[0])
+    _vector(taken, "taken", 1)
+    stride, max_pages = _table(dev, table, cached, B)
+    lens, starts, slots, positions, out = torch.empty(2 * B + 2 + 2 * tokens, dtype=torch.int32, device=dev).split(
+        [B, B + 1, tokens, tokens, 1])
+    if taken_out is not None:
+        _vector(taken_out, "taken_out", 1)
+        out = taken_out
+    _on(dev, added=added, free_pages=free_pages, taken=taken, taken_out=taken_out)
+    p_ws, n_ws = _page_ws(ws, _STATUS_BYTES, dev)
+    _lib.check(_lib.load().mova_page_map(
+        cached.data_ptr(), added.data_ptr(), B, table.data_ptr(), stride, max_pages, free_pages.data_ptr(),
+        free_pages.shape[0], taken.data_ptr(), page_size, num_pages, tokens, lens.data_ptr(), starts.data_ptr(),
+        slots.data_ptr(), positions.data_ptr(), out.data_ptr(), p_ws, n_ws, _current_stream_handle()),
+        "mova_page_map")
+    return lens, starts, slots, positions, out
+
+
+def page_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+               k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+               ws: Optional[torch.Tensor] = None) -> None:
+    """Writes the keys and values of T tokens into the cache at `slots`
+    (mova_page_write): k and v (T, KV heads, 128) or (T, KV heads * 128), v as
+    value_routed returns it.  Slots of -1 are skipped."""
+    if _elsewhere(k):
+        with torch.cuda.device(k.device):
+            return page_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, ws)
+    dev, T = k.device, k.shape[0]
+    p, _, kv, _ = _pages(dev, k_cache, v_cache, k_scale, v_scale)
+    io = _CACHE_IO[k_cache.dtype]
+    if k.dtype != io or v.dtype != io:
+        raise ValueError(f"k, v: {k.dtype}, {v.dtype}; a {k_cache.dtype} cache takes {io}")
+    k_stride, v_stride = _row_stride(k, "k", kv * 128), _row_stride(v, "v", kv * 128)
+    if v.shape[0] != T:
+        raise ValueError(f"v: {v.shape[0]} tokens, expected {T}")
+    _vector(slots, "slots", T)
+    _on(dev, v=v, slots=slots)
+    p_ws, n_ws = _page_ws(ws, _STATUS_BYTES, dev)
+    _lib.check(_lib.load().mova_page_write(k.data_ptr(), v.data_ptr(), _DT[io], k_stride, v_stride, slots.data_ptr(),
+                                           T, ctypes.addressof(p), p_ws, n_ws, _current_stream_handle()),
+               "mova_page_write")
+
+
+def _bounds(dev, k_lo, k_hi, num: int, kv: int, dtype) -> None:
+    for name, t in (("k_lo", k_lo), ("k_hi", k_hi)):
+        if t.dtype != dtype or t.shape != (num, kv, 128) or not t.is_contiguous():
+            raise ValueError(f"{name}: expected contiguous {dtype} of shape {(num, kv, 128)}, got {t.dtype} "
+                             f"{tuple(t.shape)}")
+    _on(dev, k_lo=k_lo, k_hi=k_hi)
+
+
+def page_bounds(k_cache: torch.Tensor, table: torch.Tensor, cached: torch.Tensor, lens: torch.Tensor,
+                k_lo: torch.Tensor, k_hi: torch.Tensor, ws: Optional[torch.Tensor] = None) -> None:
+    """Updates the per-page key bounds k_lo, k_hi (num_pages, KV heads, 128)
+    of the pages that the step from `cached` to `lens` tokens has filled
+    (mova_page_bounds)."""
+    if _elsewhere(k_cache):
+        with torch.cuda.device(k_cache.device):
+            return page_bounds(k_cache, table, cached, lens, k_lo, k_hi, ws)
+    dev, B = k_cache.device, lens.shape[0]
+    p, num, kv, _ = _pages(dev, k_cache)
+    stride, max_pages = _table(dev, table, lens, B)
+    _vector(cached, "cached", B)
+    _on(dev, cached=cached)
+    _bounds(dev, k_lo, k_hi, num, kv, k_cache.dtype)
+    p_ws, n_ws = _page_ws(ws, _STATUS_BYTES, dev)
+    _lib.check(_lib.load().mova_page_bounds(ctypes.addressof(p), table.data_ptr(), stride, max_pages,
+                                            cached.data_ptr(), lens.data_ptr(), B, k_lo.data_ptr(), k_hi.data_ptr(),
+                                            p_ws, n_ws, _current_stream_handle()), "mova_page_bounds")
+
+
+def page_select(q: torch.Tensor, k_lo: torch.Tensor, k_hi: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                page_size: int, top: int, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The `top` pages of each request that a bound on the scores ranks first,
+    the last page always among them (mova_page_select): (B, KV heads, top)
+    int32 page numbers within the request, ascending, then -1.  q (B, H, 128)."""
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return page_select(q, k_lo, k_hi, table, lens, page_size, top, ws)
+    dev = q.device
+    if k_lo.dtype not in _CACHE_IO or k_lo.dim() != 3:
+        raise ValueError(f"k_lo: expected (num_pages, KV heads, 128) of a cache's dtype, got {k_lo.dtype} "
+                         f"{tuple(k_lo.shape)}")
+    num, kv, _ = k_lo.shape
+    _bounds(dev, k_lo, k_hi, num, kv, k_lo.dtype)
+    _heads(q, "q", _CACHE_IO[k_lo.dtype])
+    B, H, _ = q.shape
+    q_stride = _row_stride(q, "q", H * 128)
+    stride, max_pages = _table(dev, table, lens, B)
+    picked = torch.empty((B, kv, top), dtype=torch.int32, device=dev)
+    p = _lib.Pages(0, 0, _DT[k_lo.dtype], num, kv, page_size, 0, 0, 0, 0)
+    p_ws, n_ws = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
+    _lib.check(_lib.load().mova_page_select(q.data_ptr(), _DT[q.dtype], q_stride, H, ctypes.addressof(p),
+                                            k_lo.data_ptr(), k_hi.data_ptr(), table.data_ptr(), stride, max_pages,
+                                            lens.data_ptr(), B, top, picked.data_ptr(), p_ws, n_ws,
+                                            _current_stream_handle()), "mova_page_select")
+    return picked
+
+
+def page_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                lens: torch.Tensor, scale: Optional[float] = None, picked: Optional[torch.Tensor] = None,
+                k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                return_lse: bool = False, out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Attention of one new token per request over its cached tokens
+    (mova_page_attend): o (B, H, 128) in q's dtype [, lse (B, H) fp32], zeros
+    (and -inf) for requests of length 0.  scale defaults to 1 / sqrt(128).
+    picked (B, KV heads, top): only these pages, from page_select."""
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return page_attend(q, k_cache, v_cache, table, lens, scale, picked, k_scale, v_scale, return_lse, out, ws)
+    dev = q.device
+    p, _, kv, _ = _pages(dev, k_cache, v_cache, k_scale, v_scale)
+    _heads(q, "q", _CACHE_IO[k_cache.dtype])
+    B, H, _ = q.shape
+    q_stride = _row_stride(q, "q", H * 128)
+    stride, max_pages = _table(dev, table, lens, B)
+    p_picked = top = 0
+    if picked is not None:
+        if picked.dtype != torch.int32 or picked.dim() != 3 or picked.shape[:2] != (B, kv) or not picked.is_contiguous():
+            raise ValueError(f"picked: expected contiguous int32 of shape ({B}, {kv}, top), got {picked.dtype} "
+                             f"{tuple(picked.shape)}")
+        _on(dev, picked=picked)
+        p_picked, top = picked.data_ptr(), picked.shape[2]
+    if out is None:
+        out = torch.empty((B, H, 128), dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError(f"out: expected contiguous {q.dtype} of shape {tuple(q.shape)}")
+    else:
+        _on(dev, out=out)
+    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if return_lse else None
+    p_ws, n_ws = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
+    _lib.check(_lib.load().mova_page_attend(
+        q.data_ptr(), _DT[q.dtype], q_stride, H, ctypes.addressof(p), table.data_ptr(), stride, max_pages,
+        lens.data_ptr(), B, 0.08838834764831845 if scale is None else scale, p_picked, top, out.data_ptr(),
+        lse.data_ptr() if return_lse else None, p_ws, n_ws, _current_stream_handle()), "mova_page_attend")
+    return (out, lse) if return_lse else out
 
 
 def workspace_parts(T: int, d: int, E: int, k: int, n: int) -> dict:

@@ -1,0 +1,770 @@
+// Attention of one new token per request over a paged key-value cache.
+//
+//   o[b, h] = sum_i p_i v_i / sum_i p_i,   p_i = exp(scale * q[b, h] . k_i)
+//
+// over the request's tokens, or over those of given pages.  Per cached token
+// and KV head the kernel reads 2 x 128 elements and does 4 * 128 * G
+// operations, G <= 16: far below the tensor cores' rate at any G, so the
+// bytes of K and V bound it and every step below serves the memory stream.
+//
+// Split.  The units of work -- 64 keys (bf16), 128 (E4M3) or 32 (fp32) of one
+// (request, KV head) -- are laid out in one line, request by request and
+// head by head, and each of the resident CTAs takes an equal, contiguous
+// share.  Lengths are known on the device only, so every CTA scans them
+// itself.  A CTA that covers a (request, head) alone writes its output; where
+// several share one, each leaves a partial result (running maximum, sum, and
+// unnormalised output) and the second kernel joins them in the order of the
+// keys.  A CTA has at most two partial results, its first and its last, so
+// the workspace does not grow with the batch.
+//
+// Stream.  Each warp owns every fourth tile of its CTA's units and a ring of
+// kStages 8 KB stages (K and V of one tile) that it fills with 16-byte
+// asynchronous copies, a few tiles ahead and across (request, head)
+// boundaries, so the stream does not stop where a softmax ends.  Page numbers
+// are looked up 32 tiles at a time, one per lane.  Tokens past the end and
+// pages that are none are filled with zeros and their scores set to -inf.
+//
+// Mathematics.  bf16: S^T = K q^T and O^T = V^T P^T on mma.m16n8k16, keys (or
+// dimensions) as the 16 rows and query heads as the 8 columns, so that G <= 8
+// heads need one column tile; one mma takes 16 keys, which tcgen05's
+// 128-row tiles would need 8 tiles of one page table for.  Scores, maxima,
+// sums and outputs are fp32.  P enters the second product as two bf16 terms
+// (p = hi + lo, relative error 2^-16): one term would add an error as large
+// as the output's own rounding.  E4M3: K, V become fp16 exactly; q is scaled
+// by a power of two to [1, 2) at its largest element and rounded to fp16
+// (exact for elements down to 2^-14 of the largest); P in fp16 (2^-11 against
+// the output's 2^-8).  fp32: plain FMAs, whose rate is enough for 8 bytes per
+// token, head and dimension.
+#include <math.h>
+
+#include <type_traits>
+
+#include "paged.cuh"
+
+namespace mova {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStages = 3;
+constexpr int kStageBytes = 8192;
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kPadDim = kHeadDim + 4;  // merge rows, padded against bank conflicts
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum Mode { kF32 = 0, kB16 = 1, kE8 = 2 };
+
+template <int M> struct Tile;  // of one warp
+template <> struct Tile<kF32> { using E = float;         static constexpr int keys = 8;  static constexpr int groups = 1; };
+template <> struct Tile<kB16> { using E = __nv_bfloat16; static constexpr int keys = 16; static constexpr int groups = 1; };
+template <> struct Tile<kE8>  { using E = uint8_t;       static constexpr int keys = 32; static constexpr int groups = 2; };
+
+struct AttendArgs {
+  PageArgs a;
+  const void* q;
+  long long q_stride;
+  int G;
+  float scale;
+  const int32_t* picked;
+  int top;
+  void* o;
+  float* lse;
+  int32_t* bad;
+  int32_t* prefix;
+  float* part;
+};
+
+// Units of request b: of its tokens, or of the picked pages' places.
+__device__ __forceinline__ int places_of(const AttendArgs& s, int len) {
+  if (s.picked == nullptr) return len;
+  const int pages = (len + (1 << s.a.shift) - 1) >> s.a.shift;
+  return (pages < s.top ? pages : s.top) << s.a.shift;
+}
+
+__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+template <int M>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (M == kB16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two E4M3 values (low 16 bits of x, or high) as fp16, exactly.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// 2^x for a score below the running maximum (x <= 0, or NaN).
+__device__ __forceinline__ float ex2(float x) { return exp2f(x); }
+// The maximum to subtract: 0 while nothing has been seen.
+__device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// One warp's softmax state for up to NT x 8 heads (mma) or NT heads (fp32).
+// mma: column heads nt * 8 + 2 * (lane & 3) + {0, 1}; fp32: all heads.
+template <int M, int NT> struct State {
+  float o[M == kF32 ? 1 : 8][NT][4];
+  float m[NT][2], l[NT][2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (M == kF32 ? 1 : 8); ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][n][c] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+  }
+};
+
+// The query heads of one KV head as mma column operands, and the factor from
+// a raw product to a base-2 exponent for this thread's columns.
+template <int M, int NT> struct Query {
+  uint32_t b[8][NT][2];
+  float f[NT][2];
+};
+
+template <int M, int NT>
+__device__ __forceinline__ void load_query(Query<M, NT>& r, const __nv_bfloat16* q, int G, float scale, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int head = n * 8 + g;
+    const __nv_bfloat16* row = q + head * kHeadDim;
+    if constexpr (M == kB16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        r.b[k][n][0] = head < G ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 2 * t) : 0u;
+        r.b[k][n][1] = head < G ? *reinterpret_cast<const uint32_t*>(row + 16 * k + 2 * t + 8) : 0u;
+      }
+      r.f[n][0] = r.f[n][1] = scale;
+    } else {
+      uint2 raw[8];
+      float big = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        raw[k] = head < G ? *reinterpret_cast<const uint2*>(row + 16 * k + 4 * t) : make_uint2(0u, 0u);
+        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[k].x));
+        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[k].y));
+        big = fmaxf(fmaxf(big, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(y.x), fabsf(y.y)));
+      }
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+      // Power of two 2^e <= big; an infinite or subnormal row keeps a factor in range.
+      int e = static_cast<int>(__float_as_uint(big) >> 23);
+      e = e < 1 ? 127 : (e > 253 ? 253 : e);
+      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+      const float up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[k].x));
+        const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&raw[k].y));
+        r.b[k][n][0] = pack_f16(x.x * down, x.y * down);
+        r.b[k][n][1] = pack_f16(y.x * down, y.y * down);
+      }
+      r.f[n][0] = scale * __shfl_sync(0xffffffffu, up, (2 * t) * 4);
+      r.f[n][1] = scale * __shfl_sync(0xffffffffu, up, (2 * t + 1) * 4);
+    }
+  }
+}
+
+// Softmax of 16 keys' scores (rows g, g + 8 of the fragment): updates the
+// state, and returns P^T as the second product's column operand.
+template <int M, int NT>
+__device__ __forceinline__ void softmax16(State<M, NT>& st, float (&s)[NT][4], const Query<M, NT>& q, int valid,
+                                          int lane, uint32_t (&p)[NT][2], uint32_t (&plo)[NT][2]) {
+  const int g = lane >> 2;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float x[4];
+    x[0] = g < valid ? s[n][0] * q.f[n][0] : -INFINITY;
+    x[1] = g < valid ? s[n][1] * q.f[n][1] : -INFINITY;
+    x[2] = g + 8 < valid ? s[n][2] * q.f[n][0] : -INFINITY;
+    x[3] = g + 8 < valid ? s[n][3] * q.f[n][1] : -INFINITY;
+    float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+      top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
+    }
+    const bool up = top[0] > st.m[n][0] || top[1] > st.m[n][1];
+    if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const float m = fmaxf(st.m[n][c], top[c]);
+        const float a = ex2(st.m[n][c] - ref_of(m));
+        st.m[n][c] = m;
+        st.l[n][c] *= a;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          st.o[i][n][c] *= a;
+          st.o[i][n][c + 2] *= a;
+        }
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = ex2(x[c] - ref_of(st.m[n][c & 1]));
+    st.l[n][0] += x[0] + x[2];
+    st.l[n][1] += x[1] + x[3];
+    if constexpr (M == kB16) {
+      // hi: the upper 16 bits (p truncated); lo: the rest, kept above zero so that
+      // an infinite value's products with both have one sign.
+      float lo[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        lo[c] = fmaxf(x[c] - __uint_as_float(__float_as_uint(x[c]) & 0xffff0000u), x[c] * 0x1p-24f);
+      p[n][0] = transpose8x8(__byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x7632));
+      p[n][1] = transpose8x8(__byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x7632));
+      plo[n][0] = transpose8x8(pack_bf16(lo[0], lo[1]));
+      plo[n][1] = transpose8x8(pack_bf16(lo[2], lo[3]));
+    } else {
+      p[n][0] = transpose8x8(pack_f16(x[0], x[1]));
+      p[n][1] = transpose8x8(pack_f16(x[2], x[3]));
+    }
+  }
+}
+
+// One tile of 16 bf16 keys: K rows of 256 bytes at `kt`, V rows at `vt`,
+// 16-byte chunk c of row r at place c ^ (r & 7).
+template <int NT>
+__device__ __forceinline__ void tile_b16(State<kB16, NT>& st, const Query<kB16, NT>& q, uint32_t kt, uint32_t vt,
+                                         int valid, int lane) {
+  const int r8 = lane & 7;
+  float s[2][NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[0][n][c] = s[1][n][c] = 0.0f;
+  const uint32_t krow = kt + (r8 + (lane & 8)) * 256;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint32_t a[4];
+    ldsm4(a, krow + (((2 * k + (lane >> 4)) ^ r8) << 4));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma16816<kB16>(s[k & 1][n], a[0], a[1], a[2], a[3], q.b[k][n][0], q.b[k][n][1]);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[0][n][c] += s[1][n][c];
+  uint32_t p[NT][2], plo[NT][2];
+  softmax16<kB16, NT>(st, s[0], q, valid, lane, p, plo);
+  const uint32_t vrow = vt + (r8 + ((lane >> 4) << 3)) * 256;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t a[4];
+    ldsm4t(a, vrow + (((2 * i + ((lane >> 3) & 1)) ^ r8) << 4));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      mma16816<kB16>(st.o[i][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
+      mma16816<kB16>(st.o[i][n], a[0], a[1], a[2], a[3], plo[n][0], plo[n][1]);
+    }
+  }
+}
+
+// One tile of 32 E4M3 keys: rows of 128 bytes, chunk c of row r at c ^ (r & 7).
+// A 32-bit word of a row fragment holds dimensions 16 c + 4 t + {0..3} of row
+// g: the first two are the product's k = 2t, 2t + 1, the others k = 2t + 8,
+// 2t + 9 (load_query orders q alike).  A transposed V fragment holds
+// dimensions 16 c + 2 g + {0, 1} of keys 2t, 2t + 1: the even dimension is
+// row g of the output tile, the odd one row g + 8.
+template <int NT>
+__device__ __forceinline__ void tile_e8(State<kE8, NT>& st, const Query<kE8, NT>& q, uint32_t kt, uint32_t vt,
+                                        int valid0, int valid1, int lane) {
+  const int r8 = lane & 7;
+  float s[2][NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s[0][n][c] = s[1][n][c] = 0.0f;
+  // Matrices: rows 0-7, 8-15 (first 16 keys), 16-23, 24-31 (second), one chunk.
+  const uint32_t krow = kt + (r8 + ((lane >> 3) << 3)) * 128;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uint32_t a[4];
+    ldsm4(a, krow + ((k ^ r8) << 4));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a0 = e4m3_lo(a[2 * h]), a1 = e4m3_lo(a[2 * h + 1]);
+      const uint32_t a2 = e4m3_hi(a[2 * h]), a3 = e4m3_hi(a[2 * h + 1]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816<kE8>(s[h][n], a0, a1, a2, a3, q.b[k][n][0], q.b[k][n][1]);
+    }
+  }
+  uint32_t p[2][NT][2], none[NT][2];
+  softmax16<kE8, NT>(st, s[0], q, valid0, lane, p[0], none);
+  // The second half's maximum may rescale the first half's output: not yet
+  // added, so its probabilities are formed against the final maximum instead.
+  float before[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) before[n][0] = st.m[n][0], before[n][1] = st.m[n][1];
+  softmax16<kE8, NT>(st, s[1], q, valid1, lane, p[1], none);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const bool moved = before[n][0] != st.m[n][0] || before[n][1] != st.m[n][1];
+    if (__any_sync(0xffffffffu, moved)) {
+      const int g = lane >> 2;
+      float x[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool in = (c < 2 ? g : g + 8) < valid0;
+        x[c] = in ? ex2(s[0][n][c] * q.f[n][c & 1] - ref_of(st.m[n][c & 1])) : 0.0f;
+      }
+      p[0][n][0] = transpose8x8(pack_f16(x[0], x[1]));
+      p[0][n][1] = transpose8x8(pack_f16(x[2], x[3]));
+    }
+  }
+  const uint32_t vrow = vt + (r8 + ((lane >> 3) << 3)) * 128;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t a[4];
+    ldsm4t(a, vrow + ((i ^ r8) << 4));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t x = __byte_perm(a[2 * h], 0, 0x3120), y = __byte_perm(a[2 * h + 1], 0, 0x3120);
+      const uint32_t a0 = e4m3_lo(x), a1 = e4m3_hi(x), a2 = e4m3_lo(y), a3 = e4m3_hi(y);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma16816<kE8>(st.o[i][n], a0, a1, a2, a3, p[h][n][0], p[h][n][1]);
+    }
+  }
+}
+
+// One tile of 8 fp32 keys: rows of 512 bytes, chunk c of row r at
+// c ^ ((r & 1) << 2).  Scores: four lanes per key, 32 dimensions each; then
+// each lane holds dimensions 4 * lane + {0..3} of the output.  NT heads.
+template <int NT>
+__device__ __forceinline__ void tile_f32(State<kF32, NT>& st, const float* q, float scale, const char* kt,
+                                         const char* vt, int valid, int lane) {
+  const int key = lane >> 2, part = lane & 3;
+  float s[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) s[n] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c = part + 4 * i;
+    const float4 k = *reinterpret_cast<const float4*>(kt + key * 512 + ((c ^ ((key & 1) << 2)) << 4));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float4 x = *reinterpret_cast<const float4*>(q + n * kHeadDim + 4 * c);
+      s[n] = fmaf(k.w, x.w, fmaf(k.z, x.z, fmaf(k.y, x.y, fmaf(k.x, x.x, s[n]))));
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    s[n] += __shfl_xor_sync(0xffffffffu, s[n], 1);
+    s[n] += __shfl_xor_sync(0xffffffffu, s[n], 2);
+    const float x = key < valid ? s[n] * scale : -INFINITY;
+    float top = x;
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float m = fmaxf(st.m[n][0], top);
+    const float a = ex2(st.m[n][0] - ref_of(m));
+    st.m[n][0] = m;
+    s[n] = ex2(x - ref_of(m));
+    st.l[n][0] = st.l[n][0] * a + s[n];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) st.o[0][n][c] *= a;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 v = *reinterpret_cast<const float4*>(vt + j * 512 + ((lane ^ ((j & 1) << 2)) << 4));
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float p = __shfl_sync(0xffffffffu, s[n], 4 * j);
+      st.o[0][n][0] = fmaf(p, v.x, st.o[0][n][0]);
+      st.o[0][n][1] = fmaf(p, v.y, st.o[0][n][1]);
+      st.o[0][n][2] = fmaf(p, v.z, st.o[0][n][2]);
+      st.o[0][n][3] = fmaf(p, v.w, st.o[0][n][3]);
+    }
+  }
+}
+
+// First unit of worker w of W <= U, U units in all; and the worker of unit u.
+// Every worker has a unit, so every one between a row's first and last
+// leaves a partial result.
+__device__ __forceinline__ int first_unit(int w, int W, int U) {
+  return static_cast<int>(static_cast<long long>(w) * U / W);
+}
+__device__ __forceinline__ int worker_of(int u, int W, int U) {
+  return static_cast<int>((static_cast<long long>(u + 1) * W - 1) / U);
+}
+
+// Dynamic shared memory: the ring, the merge rows of kWarps x G heads, the
+// fp32 queries, and the prefix.
+template <int M>
+__host__ __device__ constexpr size_t attend_smem(int G, int B) {
+  return kRingBytes + static_cast<size_t>(kWarps) * G * kPadDim * 4 + (M == kF32 ? kMaxGroup * kHeadDim * 4 : 0) +
+         static_cast<size_t>(B + 1) * 4;
+}
+
+// NT: mma column tiles of 8 heads, or fp32 heads.
+template <int M, int NT>
+__global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs s) {
+  using E = typename Tile<M>::E;
+  using Out = typename std::conditional<M == kF32, float, __nv_bfloat16>::type;
+  constexpr int kKeys = Tile<M>::keys;
+  constexpr int kGroups = Tile<M>::groups;
+  constexpr int kUnit = kWarps * kKeys;
+  constexpr int kRow = kHeadDim * sizeof(E);      // bytes of a key
+  constexpr int kChunks = kRow / 16;
+  extern __shared__ __align__(128) char smem[];
+  __shared__ float sm_m[kWarps][kMaxGroup], sm_l[kWarps][kMaxGroup];
+  __shared__ int sm_valid[kWarps][kStages][2];
+  __shared__ int sm_bad;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = s.G, kv = s.a.kv, B = s.a.B, shift = s.a.shift;
+  float* merge = reinterpret_cast<float*>(smem + kRingBytes);
+  float* q_sm = merge + kWarps * G * kPadDim;
+  int* pre = reinterpret_cast<int*>(q_sm + (M == kF32 ? kMaxGroup * kHeadDim : 0));
+  const int w = blockIdx.x;
+
+  if (tid == 0) sm_bad = kNoBad;
+  pdl_wait();
+  pdl_trigger();
+  __syncthreads();
+  request_scan<kThreads>(B, pre, [&](int b) {
+    const int len = s.a.lens[b], use = clamp_len(len, s.a.max_pages, shift);
+    if (use != len) atomicMin(&sm_bad, b);
+    return (places_of(s, use) + kUnit - 1) / kUnit;
+  });
+  const int U = kv * pre[B];
+  if (w == 0)
+    for (int b = tid; b <= B; b += kThreads) s.prefix[b] = pre[b];
+  const int W = min(static_cast<int>(gridDim.x), U);
+  const int u0 = w < W ? first_unit(w, W, U) : 0, count = w < W ? first_unit(w + 1, W, U) - u0 : 0;
+
+  // Page lookup of 32 tiles: lane i that of tile `at + i` of this warp.
+  int t_page[kGroups], t_row[kGroups], t_valid[kGroups];
+  auto look_up = [&](int at) {
+    const int i = at + lane;
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) t_page[j] = t_row[j] = t_valid[j] = 0;
+    if (i >= count) return;
+    const int u = u0 + i;
+    const int b = request_of(pre, B, u / kv);
+    const int tiles = pre[b + 1] - pre[b], rem = u - kv * pre[b];
+    const int h = rem / tiles;
+    const int len = clamp_len(s.a.lens[b], s.a.max_pages, shift);
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      const int place = (rem - h * tiles) * kUnit + warp * kKeys + 16 * j;
+      const int in = place & ((1 << shift) - 1);
+      int page = place >> shift;
+      if (s.picked != nullptr) {
+        const int pages = (len + (1 << shift) - 1) >> shift;
+        const int listed = page < s.top && page < pages
+                               ? s.picked[(static_cast<long long>(b) * kv + h) * s.top + page] : -1;
+        page = listed < pages ? listed : -1;
+      }
+      int valid = page < 0 ? 0 : len - ((page << shift) + in);
+      valid = valid < 0 ? 0 : (valid > 16 ? 16 : valid);
+      if (valid > 0) {
+        const int id = s.a.table[b * s.a.table_stride + page];
+        if (id < 0 || id >= s.a.num_pages) {
+          atomicMin(&sm_bad, b);
+          valid = 0;
+        } else {
+          t_page[j] = id;
+          t_row[j] = (h << shift) + in;
+        }
+      }
+      t_valid[j] = valid;
+    }
+  };
+  const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
+  const char* k_base = static_cast<const char*>(s.a.k);
+  const char* v_base = static_cast<const char*>(s.a.v);
+  // Starts the copies of tile i (of this warp) into its stage.
+  auto issue = [&](int i) {
+    if ((i & 31) == 0) look_up(i);
+    if (i < count) {
+      const int stage = i % kStages;
+      const uint32_t dst = ring + stage * kStageBytes;
+#pragma unroll
+      for (int j = 0; j < kGroups; ++j) {
+        const long long page = __shfl_sync(0xffffffffu, t_page[j], i & 31);
+        const long long row = __shfl_sync(0xffffffffu, t_row[j], i & 31);
+        const int valid = __shfl_sync(0xffffffffu, t_valid[j], i & 31);
+        const char* ks = k_base + (page * s.a.k_stride + row * kHeadDim) * static_cast<long long>(sizeof(E));
+        const char* vs = v_base + (page * s.a.v_stride + row * kHeadDim) * static_cast<long long>(sizeof(E));
+        if (lane == 0) sm_valid[warp][stage][j] = valid;
+        constexpr int kRowsPer = 32 / kChunks;  // rows of one warp-wide copy
+        constexpr int kCopies = kKeys / kGroups / kRowsPer;
+        const int c = lane % kChunks;
+#pragma unroll
+        for (int x = 0; x < kCopies; ++x) {
+          const int r = x * kRowsPer + lane / kChunks;  // within the group
+          const int rr = r + 16 * j;
+          const int swz = M == kF32 ? (c ^ ((rr & 1) << 2)) : (c ^ (rr & 7));
+          const uint32_t at = dst + rr * kRow + (swz << 4);
+          const int bytes = r < valid ? 16 : 0;
+          const long long off = r < valid ? static_cast<long long>(r) * kRow + c * 16 : 0;
+          cp16_zfill(at, ks + off, bytes);
+          cp16_zfill(at + kStageBytes / 2, vs + off, bytes);
+        }
+      }
+    }
+    cp_commit();
+  };
+
+  if (count > 0) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    int b = request_of(pre, B, u0 / kv);
+    int tiles = pre[b + 1] - pre[b];
+    int h = (u0 - kv * pre[b]) / tiles;
+    int t = u0 - kv * pre[b] - h * tiles;
+    State<M, NT> st;
+    Query<M, M == kF32 ? 1 : NT> q;
+    bool fresh = true, whole = t == 0;
+    for (int i = 0; i < count; ++i) {
+      if (fresh) {
+        st.clear();
+        const long long at = b * s.q_stride + static_cast<long long>(h) * G * kHeadDim;
+        if constexpr (M == kF32) {
+          const float* src = static_cast<const float*>(s.q) + at;
+          for (int x = tid; x < NT * kHeadDim; x += kThreads) q_sm[x] = x < G * kHeadDim ? src[x] : 0.0f;
+          __syncthreads();
+        } else {
+          const float k_scale = M == kE8 && s.a.k_scale != nullptr ? s.a.k_scale[h] : 1.0f;
+          load_query<M, NT>(q, static_cast<const __nv_bfloat16*>(s.q) + at, G, s.scale * kLog2e * k_scale, lane);
+        }
+        fresh = false;
+      }
+      cp_wait<kStages - 2>();
+      __syncwarp();
+      issue(i + kStages - 1);
+      const int stage = i % kStages;
+      const uint32_t kt = ring + stage * kStageBytes, vt = kt + kStageBytes / 2;
+      if constexpr (M == kB16) {
+        tile_b16<NT>(st, q, kt, vt, sm_valid[warp][stage][0], lane);
+      } else if constexpr (M == kE8) {
+        tile_e8<NT>(st, q, kt, vt, sm_valid[warp][stage][0], sm_valid[warp][stage][1], lane);
+      } else {
+        const char* p = smem + (warp * kStages + stage) * kStageBytes;
+        tile_f32<NT>(st, q_sm, s.scale * kLog2e, p, p + kStageBytes / 2, sm_valid[warp][stage][0], lane);
+      }
+      const bool row_end = t + 1 == tiles;
+      if (row_end || i + 1 == count) {
+        // Join the four warps: maxima, sums and outputs through shared memory.
+        const int g = lane >> 2, t4 = lane & 3;
+        if constexpr (M == kF32) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float l = st.l[n][0];  // the four lanes of a key hold the same
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (n < G) {
+              if (lane == 0) sm_m[warp][n] = st.m[n][0], sm_l[warp][n] = l;
+              *reinterpret_cast<float4*>(&merge[(warp * G + n) * kPadDim + 4 * lane]) =
+                  make_float4(st.o[0][n][0], st.o[0][n][1], st.o[0][n][2], st.o[0][n][3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float l = st.l[n][c];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+              const int head = n * 8 + 2 * t4 + c;
+              if (head < G) {
+                if (g == 0) sm_m[warp][head] = st.m[n][c], sm_l[warp][head] = l;
+                float* row = &merge[(warp * G + head) * kPadDim];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                  row[16 * x + (M == kE8 ? 2 * g : g)] = st.o[x][n][c];
+                  row[16 * x + (M == kE8 ? 2 * g + 1 : g + 8)] = st.o[x][n][c + 2];
+                }
+              }
+            }
+        }
+        __syncthreads();
+        const float v_scale = M == kE8 && s.a.v_scale != nullptr ? s.a.v_scale[h] : 1.0f;
+        const bool done = whole && row_end;
+        float* part = s.part + static_cast<size_t>(w * 2 + (whole ? 1 : 0)) * (G * (kHeadDim + 2));
+        for (int head = 0; head < G; ++head) {
+          float m = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) m = fmaxf(m, sm_m[x][head]);
+          float l = 0.0f, o = 0.0f;
+#pragma unroll
+          for (int x = 0; x < kWarps; ++x) {
+            const float f = ex2(sm_m[x][head] - ref_of(m));
+            l = fmaf(sm_l[x][head], f, l);
+            o = fmaf(merge[(x * G + head) * kPadDim + tid], f, o);
+          }
+          o *= v_scale;
+          if (done) {
+            const long long at = (static_cast<long long>(b) * kv + h) * G + head;
+            static_cast<Out*>(s.o)[at * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : o / l);
+            if (s.lse != nullptr && tid == 0) s.lse[at] = (m + log2f(l)) * kLn2;
+          } else {
+            part[head * kHeadDim + tid] = o;
+            if (tid == 0) part[G * kHeadDim + head] = m, part[G * (kHeadDim + 1) + head] = l;
+          }
+        }
+        __syncthreads();
+        fresh = whole = true;
+        t = -1;
+        if (row_end && i + 1 < count) {
+          if (++h == kv) {
+            h = 0;
+            do ++b; while (pre[b + 1] == pre[b]);
+            tiles = pre[b + 1] - pre[b];
+          }
+        }
+      }
+      ++t;
+    }
+    cp_wait<0>();
+  }
+  __syncthreads();
+  if (tid == 0) s.bad[w] = sm_bad;
+}
+
+// Joins the partial results of each (request, KV head) that several workers
+// share, in the order of its keys; writes zeros where there is no token; and
+// the status.
+template <int M>
+__global__ void __launch_bounds__(kThreads) page_join_kernel(const AttendArgs s, int workers, StatusBlock* sb) {
+  using Out = typename std::conditional<M == kF32, float, __nv_bfloat16>::type;
+  __shared__ float factor[kMaxWorkers];
+  __shared__ float red[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = s.G, kv = s.a.kv, B = s.a.B;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+    int bad = kNoBad;
+    for (int i = lane; i < workers; i += 32) bad = min(bad, s.bad[i]);
+    bad = __reduce_min_sync(0xffffffffu, bad);
+    if (lane == 0) {
+      sb->code = bad == kNoBad ? MOVA_OK : MOVA_ERR_DEVICE_CHECK;
+      sb->detail = bad == kNoBad ? 0 : bad;
+    }
+  }
+  const int b = blockIdx.x / kv, h = blockIdx.x - b * kv;
+  const int p0 = s.prefix[b], tiles = s.prefix[b + 1] - p0, U = kv * s.prefix[B];
+  const int W = min(workers, U);
+  const int first = blockIdx.y, step = gridDim.y;
+  const long long at0 = static_cast<long long>(blockIdx.x) * G;
+  Out* o = static_cast<Out*>(s.o);
+  if (tiles == 0) {
+    for (int head = first; head < G; head += step) {
+      o[(at0 + head) * kHeadDim + tid] = from_f32<Out>(0.0f);
+      if (s.lse != nullptr && tid == 0) s.lse[at0 + head] = -INFINITY;
+    }
+    return;
+  }
+  const int u0 = kv * p0 + h * tiles;
+  const int w0 = worker_of(u0, W, U), parts = worker_of(u0 + tiles - 1, W, U) - w0 + 1;
+  if (parts == 1) return;
+  const size_t size = static_cast<size_t>(G) * (kHeadDim + 2);
+  // Worker w0 begins this row (its second place), the others continue it.
+  auto part = [&](int i) { return s.part + (static_cast<size_t>(w0 + i) * 2 + (i == 0 ? 1 : 0)) * size; };
+  for (int head = first; head < G; head += step) {
+    float m = -INFINITY;
+    for (int i = tid; i < parts; i += kThreads) m = fmaxf(m, part(i)[G * kHeadDim + head]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kThreads / 32; ++x) m = fmaxf(m, red[x]);
+    for (int i = tid; i < parts; i += kThreads) factor[i] = ex2(part(i)[G * kHeadDim + head] - ref_of(m));
+    __syncthreads();
+    float l = 0.0f, acc = 0.0f;
+#pragma unroll 8
+    for (int i = 0; i < parts; ++i) {
+      l = fmaf(part(i)[G * (kHeadDim + 1) + head], factor[i], l);
+      acc = fmaf(part(i)[head * kHeadDim + tid], factor[i], acc);
+    }
+    o[(at0 + head) * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : acc / l);
+    if (s.lse != nullptr && tid == 0) s.lse[at0 + head] = (m + log2f(l)) * kLn2;
+    __syncthreads();
+  }
+}
+
+template <int M, int NT>
+cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
+  auto kern = page_attend_kernel<M, NT>;
+  static bool done[64] = {false};
+  cudaError_t err = allow_smem(kern, attend_smem<M>(kMaxGroup, kMaxRequests), done);
+  if (err != cudaSuccess) return err;
+  const size_t smem = attend_smem<M>(s.G, s.a.B);
+  const int per_sm = 2 * (smem + 2048) <= 227 * 1024 ? 2 : 1;
+  const long long most = static_cast<long long>(s.a.B) * s.a.kv *
+                         (((static_cast<long long>(s.a.max_pages) << s.a.shift) + kWarps * Tile<M>::keys - 1) /
+                          (kWarps * Tile<M>::keys));
+  long long W = static_cast<long long>(sm_count()) * per_sm;
+  if (W > kMaxWorkers) W = kMaxWorkers;
+  if (W > most) W = most < 1 ? 1 : most;
+  err = launch_pdl(kern, dim3(static_cast<unsigned>(W)), dim3(kThreads), smem, stream, s);
+  if (err != cudaSuccess) return err;
+  const int rows = s.a.B * s.a.kv;
+  return launch_pdl(page_join_kernel<M>, dim3(rows, rows * s.G <= 4096 ? s.G : 1), dim3(kThreads), 0, stream, s,
+                    static_cast<int>(W), sb);
+}
+
+}  // namespace
+
+cudaError_t launch_page_attend(const void* q, long long q_stride, int G, const PageArgs& a, mova_dtype dt, float scale,
+                               const int32_t* picked, int top, void* o, float* lse, const PageWs& ws,
+                               cudaStream_t stream) {
+  const AttendArgs s{a, q, q_stride, G, scale, picked, top, o, lse, ws.bad, ws.prefix, ws.part};
+  if (dt == MOVA_F32) {
+    if (G <= 4) return launch_attend_t<kF32, 4>(s, ws.sb, stream);
+    if (G <= 8) return launch_attend_t<kF32, 8>(s, ws.sb, stream);
+    return launch_attend_t<kF32, 16>(s, ws.sb, stream);
+  }
+  if (dt == MOVA_BF16) {
+    if (G <= 8) return launch_attend_t<kB16, 1>(s, ws.sb, stream);
+    return launch_attend_t<kB16, 2>(s, ws.sb, stream);
+  }
+  if (G <= 8) return launch_attend_t<kE8, 1>(s, ws.sb, stream);
+  return launch_attend_t<kE8, 2>(s, ws.sb, stream);
+}
+
+}  // namespace mova

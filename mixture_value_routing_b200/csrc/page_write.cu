@@ -1,0 +1,276 @@
+// Writing new tokens into cache pages, and the pages' key bounds.
+//
+// page_write: cache[slot / page_size, h, slot % page_size, :] = k[t, h, :] (v
+// alike), converted to the pages' type; E4M3 as round(k / scale), the quotient
+// formed in fp32 (IEEE division) and clamped to +-448.  Each element is read
+// and written once: a copy, bound by memory.  A warp takes one token's keys or
+// values -- kv_heads * 128 elements, contiguous on the input side and 128 at a
+// time in the cache -- with 16-byte loads that do not wait for the slot.
+//
+// page_bounds: lo / hi[page, h, d] = min / max over the page's keys, for pages
+// that the step filled: page_size * 128 elements read for 256 written, bound
+// by memory; one CTA per (page, head), all its loads in flight at once.
+#include <math.h>
+
+#include "paged.cuh"
+
+namespace mova {
+
+namespace {
+
+constexpr int kWriteThreads = 256;
+
+template <typename In> constexpr int per_chunk() { return 16 / sizeof(In); }
+
+__device__ __forceinline__ uint8_t to_e4m3(float x, float scale) {
+  const float y = __fdiv_rn(x, scale);
+  return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Stores one 16-byte input chunk at element `at` of the cache.
+__device__ __forceinline__ void store_chunk(float* cache, long long at, const uint4& x, float) {
+  *reinterpret_cast<uint4*>(cache + at) = x;
+}
+__device__ __forceinline__ void store_chunk(__nv_bfloat16* cache, long long at, const uint4& x, float) {
+  *reinterpret_cast<uint4*>(cache + at) = x;
+}
+__device__ __forceinline__ void store_chunk(uint8_t* cache, long long at, const uint4& x, float scale) {
+  const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&x);
+  uint32_t out[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    out[i >> 2] |= static_cast<uint32_t>(to_e4m3(__bfloat162float(e[i]), scale)) << (8 * (i & 3));
+  *reinterpret_cast<uint2*>(cache + at) = make_uint2(out[0], out[1]);
+}
+
+template <typename In, typename Out>
+__global__ void __launch_bounds__(kWriteThreads)
+page_write_kernel(const In* __restrict__ k, const In* __restrict__ v, long long k_stride, long long v_stride,
+                  const int32_t* __restrict__ slots, int T, Out* __restrict__ kc, Out* __restrict__ vc,
+                  long long kp_stride, long long vp_stride, const float* k_scale, const float* v_scale, int kv,
+                  int shift, int num_slots, int lanes, StatusBlock* sb) {
+  constexpr int kPer = per_chunk<In>();
+  constexpr int kUnroll = 4;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  if (blockIdx.x == gridDim.x - 1) {
+    // The last CTA only looks the slots over and writes the status.
+    __shared__ int bad;
+    if (tid == 0) bad = kNoBad;
+    __syncthreads();
+    int mine = kNoBad;
+#pragma unroll 8
+    for (int t = tid; t < T; t += kWriteThreads) {
+      const int slot = slots[t];
+      if (slot < -1 || slot >= num_slots) mine = min(mine, t);
+    }
+    if (mine != kNoBad) atomicMin(&bad, mine);
+    __syncthreads();
+    if (tid == 0) {
+      sb->code = bad == kNoBad ? MOVA_OK : MOVA_ERR_DEVICE_CHECK;
+      sb->detail = bad == kNoBad ? 0 : bad;
+    }
+    return;
+  }
+  // `lanes` (16 or 32) threads per (token, keys or values).
+  const long long unit = (static_cast<long long>(blockIdx.x) * kWriteThreads + tid) / lanes;
+  const int lane = tid % lanes;
+  const int t = static_cast<int>(unit >> 1);
+  if (t >= T) return;
+  const bool is_v = unit & 1;
+  const In* src = is_v ? v + t * v_stride : k + t * k_stride;
+  Out* cache = is_v ? vc : kc;
+  const float* scale = is_v ? v_scale : k_scale;
+  const int chunks = kv * (kHeadDim / kPer);
+  const int slot = slots[t];
+  const bool ok = slot >= 0 && slot < num_slots;
+  const long long base =
+      ok ? (slot >> shift) * (is_v ? vp_stride : kp_stride) + static_cast<long long>(slot & ((1 << shift) - 1)) * kHeadDim
+         : 0;
+  for (int c0 = lane; c0 < chunks; c0 += lanes * kUnroll) {
+    uint4 x[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int c = c0 + i * lanes;
+      if (c < chunks) x[i] = *reinterpret_cast<const uint4*>(src + c * kPer);
+    }
+    if (!ok) return;
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int c = c0 + i * lanes;
+      if (c < chunks) {
+        const int h = c / (kHeadDim / kPer), d = (c % (kHeadDim / kPer)) * kPer;
+        const float s = scale == nullptr ? 1.0f : scale[h];
+        store_chunk(cache, base + (static_cast<long long>(h) << shift) * kHeadDim + d, x[i], s);
+      }
+    }
+  }
+}
+
+template <typename In, typename Out>
+cudaError_t launch_write_t(const void* k, const void* v, long long k_stride, long long v_stride, const int32_t* slots,
+                           int T, const mova_pages& p, int shift, StatusBlock* sb, cudaStream_t stream) {
+  const int lanes = p.kv_heads * (kHeadDim / per_chunk<In>()) >= 32 ? 32 : 16;
+  const long long blocks = (2LL * T * lanes + kWriteThreads - 1) / kWriteThreads;
+  return launch_pdl(page_write_kernel<In, Out>, dim3(static_cast<unsigned>(blocks + 1)), dim3(kWriteThreads), 0, stream,
+                    static_cast<const In*>(k), static_cast<const In*>(v), k_stride, v_stride, slots, T,
+                    static_cast<Out*>(p.k), static_cast<Out*>(p.v), p.k_page_stride, p.v_page_stride, p.k_scale,
+                    p.v_scale, p.kv_heads, shift, p.num_pages << shift, lanes, sb);
+}
+
+// ---- Bounds --------------------------------------------------------------------
+
+constexpr int kBoundThreads = 256;
+
+// Minimum and maximum that return NaN if either operand is NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4], float) {
+  f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8], __nv_bfloat16) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __bfloat1622float2(h[i]);
+    f[2 * i] = x.x, f[2 * i + 1] = x.y;
+  }
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&f)[16], uint8_t) {
+  const uint8_t* e = reinterpret_cast<const uint8_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(e[i], __NV_E4M3)));
+}
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(uint8_t* p, float v) { *p = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
+
+template <typename E>
+__global__ void __launch_bounds__(kBoundThreads)
+page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __restrict__ lo, E* __restrict__ hi,
+                   StatusBlock* sb) {
+  constexpr int kPer = 16 / sizeof(E);
+  constexpr int kCols = kHeadDim / kPer;            // 16-byte chunks of a key
+  constexpr int kRows = kBoundThreads / kCols;      // keys of one pass
+  extern __shared__ int pre[];
+  __shared__ float red[2][kBoundThreads / 32][kHeadDim];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool checks = blockIdx.x == gridDim.x - 1;
+  __shared__ int bad;
+  if (tid == 0) bad = kNoBad;
+  pdl_wait();
+  pdl_trigger();
+  __syncthreads();
+  auto first_page = [&](int b) {
+    const int c = cached[b];
+    return (c < 0 ? 0 : c) >> a.shift;
+  };
+  request_scan<kBoundThreads>(a.B, pre, [&](int b) {
+    const int len = a.lens[b], use = clamp_len(len, a.max_pages, a.shift);
+    if (use != len || cached[b] < 0) atomicMin(&bad, b);
+    const int n = (use >> a.shift) - first_page(b);
+    return n < 0 ? 0 : n;
+  });
+  const int items = pre[a.B];
+  auto page_of = [&](int item, int* b) {
+    *b = request_of(pre, a.B, item);
+    return a.table[*b * a.table_stride + first_page(*b) + item - pre[*b]];
+  };
+  if (checks) {
+    for (int i = tid; i < items; i += kBoundThreads) {
+      int b;
+      const int page = page_of(i, &b);
+      if (page < 0 || page >= a.num_pages) atomicMin(&bad, b);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      sb->code = bad == kNoBad ? MOVA_OK : MOVA_ERR_DEVICE_CHECK;
+      sb->detail = bad == kNoBad ? 0 : bad;
+    }
+    return;
+  }
+  const int col = tid % kCols, row0 = tid / kCols;
+  const long long work = static_cast<long long>(items) * a.kv;
+  for (long long x = blockIdx.x; x < work; x += gridDim.x - 1) {
+    int b;
+    const int item = static_cast<int>(x / a.kv), h = static_cast<int>(x - static_cast<long long>(item) * a.kv);
+    const int page = page_of(item, &b);
+    if (page < 0 || page >= a.num_pages) continue;  // the same for the whole CTA
+    const E* src = static_cast<const E*>(a.k) + page * a.k_stride + (static_cast<long long>(h) << a.shift) * kHeadDim;
+    float l[kPer], u[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) l[i] = INFINITY, u[i] = -INFINITY;
+#pragma unroll 4
+    for (int r = row0; r < (1 << a.shift); r += kRows) {
+      float f[kPer];
+      unpack(*reinterpret_cast<const uint4*>(src + r * kHeadDim + col * kPer), f, E());
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) l[i] = min_nan(l[i], f[i]), u[i] = max_nan(u[i], f[i]);
+    }
+    // The rows of a warp, then the warps.
+#pragma unroll
+    for (int o = kCols; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        l[i] = min_nan(l[i], __shfl_xor_sync(0xffffffffu, l[i], o));
+        u[i] = max_nan(u[i], __shfl_xor_sync(0xffffffffu, u[i], o));
+      }
+    if (lane < kCols) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) red[0][warp][lane * kPer + i] = l[i], red[1][warp][lane * kPer + i] = u[i];
+    }
+    __syncthreads();
+    {
+      const int which = tid >> 7, d = tid & (kHeadDim - 1);
+      float m = red[which][0][d];
+#pragma unroll
+      for (int y = 1; y < kBoundThreads / 32; ++y)
+        m = which ? max_nan(m, red[1][y][d]) : min_nan(m, red[0][y][d]);
+      put((which ? hi : lo) + (static_cast<long long>(page) * a.kv + h) * kHeadDim + d, m);
+    }
+    __syncthreads();
+  }
+}
+
+template <typename E>
+cudaError_t launch_bounds_t(const PageArgs& a, const int32_t* cached, void* lo, void* hi, StatusBlock* sb,
+                            cudaStream_t stream) {
+  const long long most = static_cast<long long>(a.B) * a.max_pages * a.kv;
+  const long long grid = sm_count() * 6LL;  // 256 threads, 8 KB: six CTAs keep an SM's loads in flight
+  return launch_pdl(page_bounds_kernel<E>, dim3(static_cast<unsigned>((most < grid ? most : grid) + 1)),
+                    dim3(kBoundThreads), static_cast<size_t>(a.B + 1) * 4, stream, a, cached, static_cast<E*>(lo),
+                    static_cast<E*>(hi), sb);
+}
+
+}  // namespace
+
+cudaError_t launch_page_write(const void* k, const void* v, mova_dtype dt, long long k_stride, long long v_stride,
+                              const int32_t* slots, int T, const mova_pages& p, StatusBlock* sb, cudaStream_t stream) {
+  int shift = 0;
+  while ((1 << shift) < p.page_size) ++shift;
+  if (p.dtype == MOVA_F32)
+    return launch_write_t<float, float>(k, v, k_stride, v_stride, slots, T, p, shift, sb, stream);
+  if (p.dtype == MOVA_BF16)
+    return launch_write_t<__nv_bfloat16, __nv_bfloat16>(k, v, k_stride, v_stride, slots, T, p, shift, sb, stream);
+  (void)dt;
+  return launch_write_t<__nv_bfloat16, uint8_t>(k, v, k_stride, v_stride, slots, T, p, shift, sb, stream);
+}
+
+cudaError_t launch_page_bounds(const PageArgs& a, mova_dtype dt, const int32_t* cached, void* lo, void* hi,
+                               StatusBlock* sb, cudaStream_t stream) {
+  if (dt == MOVA_F32) return launch_bounds_t<float>(a, cached, lo, hi, sb, stream);
+  if (dt == MOVA_BF16) return launch_bounds_t<__nv_bfloat16>(a, cached, lo, hi, sb, stream);
+  return launch_bounds_t<uint8_t>(a, cached, lo, hi, sb, stream);
+}
+
+}  // namespace mova

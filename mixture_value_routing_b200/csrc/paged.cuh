@@ -1,0 +1,133 @@
+// Shared by the paged key-value cache kernels: sizes, the request scan, and
+// the launchers that page_api.cu calls.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace mova {
+
+constexpr int kHeadDim = 128;
+constexpr int kMaxRequests = 4096;
+constexpr int kMaxGroup = 16;    // query heads per KV head
+constexpr int kMaxWorkers = 640;  // CTAs of one attention call
+constexpr int kNoBad = 0x7fffffff;
+
+// Parts of the workspace that the attention kernels share.  `part` holds two
+// partial results per worker: kMaxGroup-bounded G x 128 outputs, then G
+// maxima and G sums (all fp32).
+struct PageWs {
+  StatusBlock* sb;
+  int32_t* bad;     // (kMaxWorkers + 1) first bad request seen by each worker (kNoBad: none)
+  int32_t* prefix;  // (B + 1) units of work before each request
+  float* part;
+  unsigned long long* keys;  // select: (B, kv_heads, max_pages) sortable scores
+  size_t bytes;
+};
+
+// What the kernels know of the cache.  Strides in elements.
+struct PageArgs {
+  const void* k;
+  const void* v;
+  long long k_stride, v_stride;  // page to page
+  const float* k_scale;
+  const float* v_scale;
+  int num_pages, kv, shift;  // page_size = 1 << shift
+  const int32_t* table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* lens;
+  int B;
+};
+
+// Exclusive prefix sum over the requests, by the whole CTA: pre[0..B] in
+// shared memory, count(b) evaluated once per request.  Ends with a barrier.
+template <int kThreads, typename T, typename F>
+__device__ __forceinline__ void request_scan(int B, T* pre, F count) {
+  __shared__ T warp_sum[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  T carry = 0;
+  for (int base = 0; base < B; base += kThreads) {
+    const int b = base + tid;
+    const T c = b < B ? count(b) : T(0);
+    T incl = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    T before = carry, all = carry;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const T s = warp_sum[w];
+      if (w < warp) before += s;
+      all += s;
+    }
+    if (b < B) pre[b] = before + incl - c;
+    carry = all;
+    __syncthreads();
+  }
+  if (tid == 0) pre[B] = carry;
+  __syncthreads();
+}
+
+// The last b in [0, B) with pre[b] <= x (pre[0] = 0 <= x < pre[B]).
+template <typename T>
+__device__ __forceinline__ int request_of(const T* pre, int B, T x) {
+  int lo = 0, hi = B;  // pre[lo] <= x < pre[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int clamp_len(int len, int max_pages, int shift) {
+  const long long cap = static_cast<long long>(max_pages) << shift;
+  return len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
+}
+
+// Allows `bytes` of dynamic shared memory for `kern`, once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (err == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  return err;
+}
+
+struct MapArgs {
+  const int32_t *cached, *added;
+  int B;
+  int32_t* table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* free_pages;
+  int n_free;
+  const int32_t* taken;
+  int shift, num_pages, T;
+  int32_t *lens, *starts, *slots, *positions, *taken_out;
+  StatusBlock* sb;
+};
+cudaError_t launch_page_map(const MapArgs& a, cudaStream_t stream);
+
+cudaError_t launch_page_write(const void* k, const void* v, mova_dtype dt, long long k_stride, long long v_stride,
+                              const int32_t* slots, int T, const mova_pages& p, StatusBlock* sb, cudaStream_t stream);
+cudaError_t launch_page_bounds(const PageArgs& a, mova_dtype dt, const int32_t* cached, void* lo, void* hi,
+                               StatusBlock* sb, cudaStream_t stream);
+cudaError_t launch_page_attend(const void* q, long long q_stride, int G, const PageArgs& a, mova_dtype dt, float scale,
+                               const int32_t* picked, int top, void* o, float* lse, const PageWs& ws,
+                               cudaStream_t stream);
+cudaError_t launch_page_select(const void* q, long long q_stride, int G, const PageArgs& a, mova_dtype dt,
+                               const void* lo, const void* hi, int top, int32_t* picked, const PageWs& ws,
+                               cudaStream_t stream);
+
+}  // namespace mova

@@ -1,0 +1,601 @@
+"""Paged key-value cache on the GPU, against the plain implementations and
+bounds of tests/_paged.py."""
+import math
+
+import pytest
+import torch
+
+from tests import _paged as P
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+@pytest.fixture(scope="module")
+def api():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from mixture_value_routing_b200 import build
+    build.build()
+    from mixture_value_routing_b200 import api as A
+    return A
+
+
+def ints(v):
+    return torch.tensor(v, dtype=I32, device="cuda")
+
+
+def ok(api, want=("MOVA_OK", 0)):
+    assert api.get_status() == want
+
+
+# ---- Tables and slots --------------------------------------------------------------
+
+def check_map(api, cached, added, table, free, taken, page, num, T, alias=False, wide=0):
+    want = P.page_map(cached, added, table, free, taken, page, num, T)
+    t = torch.full((len(table), len(table[0]) + wide if table else 1), -7, dtype=I32, device="cuda")
+    if table:
+        t[:, :len(table[0])] = ints(table)
+    view = t[:, :len(table[0])] if table else t
+    tk = ints([taken])
+    got = api.page_map(ints(cached), ints(added), view, ints(free), tk, page, num, T, taken_out=tk if alias else None)
+    status = api.get_status()
+    names = ("lens", "starts", "slots", "positions")
+    for name, g, w in zip(names, got, want[1:5]):
+        assert g.tolist() == w, name
+    assert view.tolist() == want[0] or not table
+    assert (t[:, len(table[0]):] == -7).all() if table else True
+    assert got[4].tolist() == [want[5]]
+    assert tk.tolist() == ([want[5]] if alias else [taken])
+    assert status == (("MOVA_OK", 0) if want[6] is None else ("MOVA_ERR_DEVICE_CHECK", want[6]))
+
+
+def test_map_by_hand(api):
+    table = [[7, -1, -1], [-1] * 3, [4, -1, -1], [-1] * 3, [-1] * 3]
+    for alias in (False, True):
+        check_map(api, [16, 0, 3, 0, 0], [2, 20, 1, 49, 0], table, [9, 8, 2, 1], 0, 16, 10, 75, alias)
+
+
+@pytest.mark.parametrize("B,page,longest,T_extra,seed", [
+    (1, 16, 1, 0, 0), (1, 256, 5000, 3, 1), (7, 16, 100, 0, 2), (64, 64, 40, 9, 3), (300, 32, 200, 100, 4),
+    (1025, 16, 3, 0, 5), (4096, 128, 9, 17, 6), (40, 64, 1700, 5, 7),
+])
+def test_map_random(api, B, page, longest, T_extra, seed):
+    g = torch.Generator().manual_seed(seed)
+    cached = (torch.randint(0, longest + 1, (B,), generator=g)).tolist()
+    added = (torch.randint(0, longest + 1, (B,), generator=g) * (torch.rand(B, generator=g) < 0.8)).tolist()
+    width = P.ceil_div(2 * longest, page) + 1
+    num = B * width + 20
+    order = torch.randperm(num, generator=g).tolist()
+    table = [[order.pop() if j < P.ceil_div(c, page) else -1 for j in range(width)] for c in cached]
+    check_map(api, cached, added, table, order, 3, page, num, sum(added) + T_extra, alias=seed % 2 == 0, wide=seed)
+
+
+@pytest.mark.parametrize("what", ["no pages left", "bad taken", "negative taken", "negative counts", "bad old page",
+                                  "bad free page", "tokens past T", "outgrows its row", "huge counts"])
+def test_map_refusals(api, what):
+    cached, added, free, taken, T, num = [5, 16, 0, 30], [3, 1, 40, 2], [1, 2, 3, 4, 5, 6], 0, 60, 10
+    table = [[7, -1, -1], [8, -1, -1], [-1] * 3, [9, 0, -1]]
+    if what == "no pages left":
+        taken = 4  # row 1 takes the fifth; row 2 wants three; row 3 wants none
+    elif what == "bad taken":
+        taken = 7
+    elif what == "negative taken":
+        taken = -1
+    elif what == "negative counts":
+        cached, added = [-5, 16, 0, 30], [3, -1, 40, 2]
+    elif what == "bad old page":
+        table[0][0] = 10
+    elif what == "bad free page":
+        free[0] = -1
+    elif what == "tokens past T":
+        T = 5
+    elif what == "outgrows its row":
+        added[1] = 40
+    else:
+        added = [2 ** 31 - 1, 2 ** 31 - 1, 40, 2]
+        cached[1] = 2 ** 31 - 1
+    check_map(api, cached, added, table, free, taken, 16, num, T)
+
+
+def test_map_without_requests_or_tokens(api):
+    check_map(api, [], [], [], [1], 0, 16, 10, 5)
+    check_map(api, [3], [0], [[1]], [], 0, 16, 10, 0)
+
+
+# ---- Writing -----------------------------------------------------------------------
+
+def check_write(api, dtype, T, kv, page, seed=0, stride_pages=0, combined=False):
+    g = torch.Generator().manual_seed(seed)
+    num = P.ceil_div(T, page) + 4
+    io, ct = P.IO[dtype], P.CACHE[dtype]
+    slots = torch.randperm(num * page, generator=g)[:T].to(I32)
+    if T > 2:
+        slots[torch.randperm(T, generator=g)[:T // 3]] = -1
+    k = torch.randn(T, 3 + kv, 128, generator=g).to(io)[:, 2:2 + kv]
+    v = torch.randn(T, kv * 128, generator=g).to(io)
+    if T:
+        k[0, 0, :6] = torch.tensor([math.nan, math.inf, -math.inf, 1e30, 0.0, -0.0]).to(io)
+    ks = 0.01 * (1 + torch.rand(kv, generator=g)) if dtype == "e4m3" else None
+    vs = 0.02 * (1 + torch.rand(kv, generator=g)) if dtype == "e4m3" else None
+    if combined:  # keys and values of a page side by side in one tensor
+        both = torch.randn(num, 2, kv, page, 128, generator=g).to(io).to(ct).cuda()
+        kc, vc = both[:, 0], both[:, 1]
+    else:
+        kc, vc = (torch.randn(num, kv, page, 128, generator=g).to(io).to(ct).cuda() for _ in range(2))
+    want = []
+    for cache, new, scale in ((kc, k, ks), (vc, v.view(T, kv, 128), vs)):
+        w = cache.cpu().clone()
+        for t in range(T):
+            if slots[t] >= 0:
+                x = new[t]
+                if scale is not None:
+                    x = (x.float() / scale[:, None]).clamp(-448, 448).to(ct)  # IEEE fp32 division; NaN stays
+                w[int(slots[t]) // page, :, int(slots[t]) % page] = x
+        want.append(w)
+    dev = [t.cuda() if t is not None else None for t in (ks, vs)]
+    kd = torch.empty(T, 3 + kv, 128, dtype=io, device="cuda")[:, 2:2 + kv].copy_(k)
+    api.page_write(kd, v.cuda(), slots.cuda(), kc, vc, *dev)
+    ok(api)
+    for cache, w in ((kc, want[0]), (vc, want[1])):
+        got = cache.cpu()
+        bits = torch.uint8 if ct == torch.float8_e4m3fn else (torch.int32 if ct == torch.float32 else torch.int16)
+        same = (got.contiguous().view(bits) == w.contiguous().view(bits)) | (got.float().isnan() & w.float().isnan())
+        assert same.all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("T,kv,page", [(1, 8, 64), (2, 1, 16), (65, 3, 32), (301, 8, 128), (700, 2, 256), (33, 13, 16)])
+def test_write(api, dtype, T, kv, page):
+    check_write(api, dtype, T, kv, page, seed=T, combined=T % 2 == 1)
+
+
+def test_write_reports_bad_slots(api):
+    kc, vc = (torch.zeros(3, 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k = torch.ones(5, 2, 128, dtype=torch.bfloat16, device="cuda")
+    api.page_write(k, k, ints([0, -1, 48, -2, 47]), kc, vc)
+    ok(api, ("MOVA_ERR_DEVICE_CHECK", 2))
+    for c in (kc, vc):
+        assert c.sum().item() == 2 * 2 * 128 and (c[0, :, 0] == 1).all() and (c[2, :, 15] == 1).all()
+    api.page_write(k, k, ints([0, 1, 2, 3, 4]), kc, vc)
+    ok(api)
+
+
+# ---- Bounds ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("lens,cached,kv,page", [
+    ([64], [0], 8, 64), ([15, 16, 17, 0, 33], [0, 0, 0, 0, 16], 2, 16), ([1000, 128, 127, 300], [500, 127, 0, 299], 3, 128),
+    ([256, 700], [0, 256], 1, 256), ([40] * 70, list(range(70)), 2, 32),
+])
+def test_bounds(api, dtype, lens, cached, kv, page):
+    s = P.make(dtype, lens, kv, 1, page, seed=len(lens))
+    if lens[0] > 60:
+        s["k"][s["table"][0, 0].item(), 0, 3, 5] = math.nan
+    lo = torch.full((s["k"].shape[0], kv, 128), 3.0).to(s["k"].dtype).cuda()
+    hi = lo.clone()
+    api.page_bounds(s["k"], s["table"], ints(cached), s["lens"], lo, hi)
+    ok(api)
+    want_lo, want_hi = torch.full(lo.shape, 3.0), torch.full(lo.shape, 3.0)
+    k = s["k"].cpu().float()
+    for b, (c, n) in enumerate(zip(cached, lens)):
+        for j in range(c // page, n // page):
+            at = s["table"][b, j].item()
+            want_lo[at], want_hi[at] = k[at].amin(1), k[at].amax(1)  # NaN where a key is NaN
+    assert torch.equal(lo.cpu().float().nan_to_num(99.0), want_lo.nan_to_num(99.0))
+    assert torch.equal(hi.cpu().float().nan_to_num(99.0), want_hi.nan_to_num(99.0))
+    assert not want_hi.isnan().all()
+
+
+def test_bounds_reports_bad_pages_and_lengths(api):
+    s = P.make("bf16", [64, 64, 64], 2, 1, 16)
+    lo = torch.zeros(s["k"].shape[0], 2, 128, dtype=torch.bfloat16, device="cuda")
+    hi = lo.clone()
+    s["table"][1, 2] = s["k"].shape[0]
+    s["table"][2, 0] = -1
+    api.page_bounds(s["k"], s["table"], ints([0, 0, 0]), s["lens"], lo, hi)
+    ok(api, ("MOVA_ERR_DEVICE_CHECK", 1))
+    assert (hi.float().abs().sum((1, 2)) > 0).sum().item() == 10
+    s = P.make("bf16", [64, 64], 2, 1, 16)
+    lo, hi = (torch.zeros(s["k"].shape[0], 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    s["lens"][1] = 1000
+    api.page_bounds(s["k"], s["table"], ints([0, 0]), s["lens"], lo, hi)
+    ok(api, ("MOVA_ERR_DEVICE_CHECK", 1))
+
+
+# ---- Attention ---------------------------------------------------------------------
+
+def check_attend(api, s, dtype, scale=None, picked=None, status=("MOVA_OK", 0), **kw):
+    o, lse = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], scale=scale, picked=picked, k_scale=s["ks"],
+                             v_scale=s["vs"], return_lse=True, **kw)
+    ok(api, status)
+    wo, wl, to, tl = P.attend(s["q"], s["k"], s["v"], s["table"], s["lens"], scale, None if picked is None else picked.cpu(),
+                              None if s["ks"] is None else s["ks"].cpu(), None if s["vs"] is None else s["vs"].cpu(), dtype)
+    err = (P.f64(o) - wo).abs()
+    assert torch.isfinite(o.float()).all()
+    assert (err <= to).all(), (err - to).max()
+    empty = wl == -math.inf
+    assert torch.equal(P.f64(lse) == -math.inf, empty)
+    assert ((P.f64(lse) - wl).abs()[~empty] <= tl[~empty]).all()
+    assert (o.cpu()[empty] == 0).all()
+    return o, lse
+
+
+EDGES = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 257, 500]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("kv,G,page", [(1, 1, 16), (2, 4, 64), (8, 4, 32), (3, 7, 128), (1, 16, 16), (2, 13, 256), (4, 8, 64),
+                                       (5, 2, 16)])
+def test_attend_edges(api, dtype, kv, G, page):
+    check_attend(api, P.make(dtype, EDGES, kv, G, page, seed=kv + G), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("lens,kv,G,page", [
+    ([1], 8, 4, 64), ([7, 0, 0], 8, 4, 16), ([20011], 2, 4, 64), ([9000, 1, 3500, 0, 12], 4, 5, 32), ([2049] * 3, 8, 1, 128),
+    ([30] * 600, 2, 3, 16),
+])
+def test_attend_lengths(api, dtype, lens, kv, G, page):
+    check_attend(api, P.make(dtype, lens, kv, G, page, seed=len(lens)), dtype)
+
+
+def test_attend_many_requests(api):
+    lens = [(7 * i) % 23 for i in range(4096)]
+    check_attend(api, P.make("bf16", lens, 1, 2, 16), "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_attend_all_rows_empty(api, dtype):
+    s = P.make(dtype, [0, 0, 0], 2, 4, 16)
+    check_attend(api, s, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_attend_layouts(api, dtype):
+    """Pages further apart than dense (keys and values in one tensor), table rows
+    of a longer table, dense q, a given output, another scale."""
+    s = P.make(dtype, [300, 77, 0, 1029], 4, 4, 64, seed=3, fused=False)
+    both = torch.stack([s["k"].view(torch.uint8), s["v"].view(torch.uint8)], 1).view(s["k"].dtype)
+    s["k"], s["v"] = both[:, 0], both[:, 1]
+    wide = torch.full((4, 50), -5, dtype=I32, device="cuda")
+    wide[:, 20:20 + s["table"].shape[1]] = s["table"]
+    s["table"] = wide[:, 20:20 + s["table"].shape[1]]
+    out = torch.empty_like(s["q"])
+    o, _ = check_attend(api, s, dtype, scale=0.31, out=out)
+    assert o is out
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_attend_large_scores(api, dtype):
+    """Scores of a few hundred: the softmax is close to picking one token, and the
+    running maximum moves."""
+    s = P.make(dtype, [1, 900, 64, 333], 2, 4, 32, seed=9)
+    s["q"] = (s["q"] * torch.linspace(1, 20, 8, device="cuda")[:, None]).to(s["q"].dtype)
+    check_attend(api, s, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_attend_growing_scores(api, dtype):
+    """The maximum grows from token to token, so every tile rescales."""
+    s = P.make(dtype, [700, 350], 1, 4, 16, seed=2)
+    s["q"] = torch.ones_like(s["q"]) / 16
+    for b, n in enumerate((700, 350)):
+        for i in range(n):
+            s["k"][s["table"][b, i // 16].item(), :, i % 16] = torch.tensor(i / n).to(s["k"].dtype)
+    check_attend(api, s, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_attend_q_of_any_size(api, dtype):
+    """Rows of q from 2^-100 to 2^100, and a row of zeros: scores stay products."""
+    s = P.make(dtype, [130, 65], 2, 4, 16, seed=4, fused=False)
+    size = torch.tensor([2.0 ** -100, 2.0 ** -20, 0.0, 1.0, 2.0 ** -130, 3.0, 2.0 ** -7, 0.5], device="cuda")
+    s["q"] = (s["q"].float() * size[:, None]).to(s["q"].dtype)
+    check_attend(api, s, dtype)
+    s["q"] = torch.full_like(s["q"], 2.0 ** 100)
+    s["k"] = torch.zeros_like(s["k"])
+    check_attend(api, s, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attend_nan_and_infinities_show(api, dtype):
+    """A NaN or infinite key or value that is attended shows in its heads' outputs,
+    as in the formula, and nowhere else."""
+    s = P.make(dtype, [40, 40, 40], 2, 2, 16, seed=5)
+    s["k"][s["table"][0, 1].item(), 0, 3, 0] = math.nan
+    s["v"][s["table"][1, 0].item(), 1, 2, 7] = math.inf
+    s["k"][s["table"][2, 0].item(), 0, 1] = math.inf  # q . k infinite or NaN
+    o, lse = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], return_lse=True)
+    ok(api)
+    assert o[0, :2].isnan().all() and lse[0, :2].isnan().all() and torch.isfinite(o[0, 2:]).all()
+    assert o[1, 2:, 7].isinf().all() and torch.isfinite(o[1, :, :7]).all() and torch.isfinite(o[1, :, 8:]).all()
+    assert not torch.isfinite(o[2, :2]).any() and torch.isfinite(o[2, 2:]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_attend_bad_pages_count_as_absent(api, dtype):
+    s = P.make(dtype, [100, 64, 48], 2, 4, 16, seed=6)
+    s["table"][1, 1] = s["k"].shape[0]
+    s["table"][2] = -1
+    check_attend(api, s, dtype, status=("MOVA_ERR_DEVICE_CHECK", 1))
+
+
+def test_attend_bad_lengths(api):
+    s = P.make("bf16", [100, 64, 48], 2, 4, 16, seed=6)
+    s["lens"][1] = -3
+    check_attend(api, s, "bf16", status=("MOVA_ERR_DEVICE_CHECK", 1))
+    s = P.make("bf16", [100, 112], 2, 4, 16, seed=6)
+    s["lens"][1] = 2 ** 31 - 1
+    check_attend(api, s, "bf16", status=("MOVA_ERR_DEVICE_CHECK", 1))
+
+
+def test_attend_far_pages(api):
+    """Pages whose element offsets pass 32 bits."""
+    num, kv, page = 9000, 8, 64
+    k = torch.empty(num, 2, kv, page, 128, dtype=torch.bfloat16, device="cuda")
+    assert k[:, 0].stride(0) * (num - 1) > 2 ** 30 and k.numel() > 2 ** 30
+    s = P.make("bf16", [200, 130], kv, 4, page, seed=8)
+    small = s["table"].clone()
+    far = torch.where((small >= 0) & (small < s["k"].shape[0]), num - 1 - small, small)
+    for x in range(s["k"].shape[0]):
+        k[num - 1 - x, 0], k[num - 1 - x, 1] = s["k"][x], s["v"][x]
+    a = api.page_attend(s["q"], s["k"], s["v"], small, s["lens"])
+    b = api.page_attend(s["q"], k[:, 0], k[:, 1], far, s["lens"])
+    ok(api)
+    assert torch.equal(a, b)
+    del k
+    num = 140000  # fp32 pages of one head: byte offsets past 2^32, element offsets past 2^31
+    k = torch.empty(num, 1, 128, 128, dtype=torch.float32, device="cuda")
+    assert k.numel() > 2 ** 31
+    s = P.make("f32", [200, 300], 1, 4, 128, seed=8)
+    small = s["table"].clone()
+    inside = (small >= 0) & (small < s["k"].shape[0])
+    far = torch.where(inside, num - 1 - small, small)
+    for x in range(s["k"].shape[0]):
+        k[num - 1 - x] = s["k"][x]
+    a = api.page_attend(s["q"], s["k"], s["k"], small, s["lens"])
+    b = api.page_attend(s["q"], k, k, far, s["lens"])
+    new = torch.randn(2, 1, 128, device="cuda")
+    api.page_write(new, new, ints([num * 128 - 1, num * 128 - 129]), k, k)
+    ok(api)
+    assert torch.equal(a, b)
+    assert torch.equal(k[-1, 0, 127], new[0, 0]) and torch.equal(k[-2, 0, 127], new[1, 0])
+
+
+# ---- Selected pages ----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_attend_given_pages(api, dtype):
+    s = P.make(dtype, [200, 33, 0, 130], 2, 4, 16, seed=11)
+    picked = torch.full((4, 2, 9), -1, dtype=I32)
+    picked[0, 0] = torch.tensor([12, 0, 5, -1, 3, 3, 11, 99, 1])  # out of order, one twice, holes, one too high
+    picked[0, 1, 4] = 7
+    picked[1, 0, :3] = torch.tensor([2, 1, 0])
+    picked[3] = torch.arange(9)
+    check_attend(api, s, dtype, picked=picked.cuda())
+
+
+def bounds_of(s, page):
+    k = s["k"].float().cpu()
+    lo = k.nan_to_num(0.0).amin(2).to(s["q"].dtype).to(s["k"].dtype).cuda()
+    return lo, k.nan_to_num(0.0).amax(2).to(s["q"].dtype).to(s["k"].dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("lens,kv,G,page,top", [
+    ([500], 2, 4, 16, 5), ([500, 16, 0, 17, 81, 1], 2, 4, 16, 1), ([500, 16, 0, 17, 81, 1], 3, 7, 16, 5),
+    ([3000, 2999, 100, 1], 1, 16, 32, 40), ([12000, 700], 2, 1, 16, 64), ([900] * 40, 2, 2, 128, 3),
+    ([33000], 1, 8, 16, 1000),
+])
+def test_select(api, dtype, lens, kv, G, page, top):
+    s = P.make(dtype, lens, kv, G, page, seed=top)
+    lo, hi = bounds_of(s, page)
+    picked = api.page_select(s["q"], lo, hi, s["table"], s["lens"], page, top)
+    ok(api)
+    assert torch.equal(picked.cpu(), P.select(s["q"], lo, hi, s["table"], s["lens"], page, top))
+    if sum(lens) < 5000:
+        check_attend(api, s, dtype, picked=picked)
+
+
+def test_select_ties_go_to_the_lower_page(api):
+    s = P.make("bf16", [16 * 100, 16 * 50], 2, 4, 16)
+    lo = torch.zeros(s["k"].shape[0], 2, 128, dtype=torch.bfloat16, device="cuda")
+    picked = api.page_select(s["q"], lo, lo, s["table"], s["lens"], 16, 7)
+    ok(api)
+    assert (picked[0].cpu() == torch.tensor([0, 1, 2, 3, 4, 5, 99])).all()
+    assert (picked[1].cpu() == torch.tensor([0, 1, 2, 3, 4, 5, 49])).all()
+    # Two values only: those with the greater, lowest first, then the others.
+    hi = lo.clone()
+    s["q"] = s["q"].abs()
+    for j in (90, 20, 30):
+        hi[s["table"][0, j].item()] = 1.0
+    picked = api.page_select(s["q"], lo, hi, s["table"], s["lens"], 16, 6)
+    assert (picked[0].cpu() == torch.tensor([0, 1, 20, 30, 90, 99])).all()
+    picked = api.page_select(s["q"], lo, hi, s["table"], s["lens"], 16, 3)
+    assert (picked[0].cpu() == torch.tensor([20, 30, 99])).all()
+
+
+def test_select_zero_signs_and_nan(api):
+    s = P.make("f32", [16 * 20], 1, 1, 16, fused=False)
+    n = s["k"].shape[0]
+    lo = torch.zeros(n, 1, 128, device="cuda")
+    hi = lo.clone()
+    hi[s["table"][0, 4].item()] = -0.0
+    s["q"] = torch.ones_like(s["q"])
+    assert api.page_select(s["q"], lo, hi, s["table"], s["lens"], 16, 6).tolist() == [[[0, 1, 2, 3, 4, 19]]]
+    lo[s["table"][0, 9].item(), 0, 3] = hi[s["table"][0, 9].item(), 0, 3] = math.nan
+    hi[s["table"][0, 7].item(), 0, 3] = math.inf
+    lo[s["table"][0, 2].item()], hi[s["table"][0, 2].item()] = -math.inf, -math.inf
+    assert api.page_select(s["q"], lo, hi, s["table"], s["lens"], 16, 3).tolist() == [[[7, 9, 19]]]
+    assert api.page_select(s["q"], lo, hi, s["table"], s["lens"], 16, 2).tolist() == [[[9, 19]]]
+    assert 2 not in api.page_select(s["q"], lo, hi, s["table"], s["lens"], 16, 19).tolist()[0][0]
+    ok(api)
+
+
+def test_select_reports_bad_pages(api):
+    s = P.make("bf16", [500, 300], 2, 4, 16)
+    lo, hi = bounds_of(s, 16)
+    s["table"][1, 3] = -9
+    picked = api.page_select(s["q"], lo, hi, s["table"], s["lens"], 16, 18)
+    ok(api, ("MOVA_ERR_DEVICE_CHECK", 1))
+    assert picked.cpu()[1].tolist() == [[j for j in range(19) if j != 3]] * 2  # counts below every other
+
+
+# ---- Streams, graphs, repetition -----------------------------------------------------
+
+def test_repeated_calls_are_bit_identical(api):
+    s = P.make("bf16", [5000, 100, 0, 2222, 64], 8, 4, 64, seed=1)
+    lo, hi = bounds_of(s, 64)
+    ws = torch.full((api.page_workspace_size(5, s["table"].shape[1], 8, 32),), 255, dtype=torch.uint8, device="cuda")
+    first = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], return_lse=True)
+    for _ in range(3):
+        picked = api.page_select(s["q"], lo, hi, s["table"], s["lens"], 64, 9, ws=ws)  # leaves the workspace changed
+        again = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], return_lse=True, ws=ws)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        assert torch.equal(picked, api.page_select(s["q"], lo, hi, s["table"], s["lens"], 64, 9))
+    assert api.get_status(ws) == ("MOVA_OK", 0)
+
+
+def test_calls_on_two_streams(api):
+    states = [P.make("bf16", [4000, 1, 300], 8, 4, 64, seed=x) for x in range(2)]
+    alone = [api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"]) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in states]
+    got = [[], []]
+    for _ in range(20):
+        for x, s in enumerate(states):
+            with torch.cuda.stream(streams[x]):
+                got[x].append(api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"]))
+    torch.cuda.synchronize()
+    for x in range(2):
+        assert all(torch.equal(g, alone[x]) for g in got[x])
+
+
+def test_captured_step_follows_its_inputs(api):
+    """One decode step captured in a graph -- page_map, page_write, page_bounds,
+    page_select and both attentions -- and replayed as the lengths grow: each
+    replay equals the step run call by call on a copy of the state."""
+    B, kv, G, page, num, width = 5, 2, 4, 16, 80, 12
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *shape: torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    def state():
+        return dict(cached=ints([0, 15, 16, 100, 0]), added=ints([1, 1, 1, 1, 0]), table=torch.zeros(B, width, dtype=I32, device="cuda"),
+                    taken=ints([10]), kc=torch.zeros(num, kv, page, 128, dtype=torch.bfloat16, device="cuda"),
+                    vc=torch.zeros(num, kv, page, 128, dtype=torch.bfloat16, device="cuda"),
+                    lo=torch.zeros(num, kv, 128, dtype=torch.bfloat16, device="cuda"),
+                    hi=torch.zeros(num, kv, 128, dtype=torch.bfloat16, device="cuda"))
+
+    free = torch.randperm(num, generator=g, device="cuda").to(I32)
+    k0, v0 = rnd(num, kv, page, 128), rnd(num, kv, page, 128)
+
+    def start(s):
+        # The requests' first pages: entries 0..9 of the free list.
+        at = 0
+        for b, n in enumerate([0, 15, 16, 100, 0]):
+            for j in range(P.ceil_div(n, page)):
+                s["table"][b, j] = free[at]
+                at += 1
+        s["kc"].copy_(k0)
+        s["vc"].copy_(v0)
+        for x, f in ((s["lo"], k0.amin(2)), (s["hi"], k0.amax(2))):
+            x.copy_(f)
+        assert at <= 10
+        return s
+
+    q, k, v = rnd(B, kv * G, 128), rnd(B, kv, 128), rnd(B, kv * 128)
+
+    def step(s):
+        lens, starts, slots, positions, _ = api.page_map(s["cached"], s["added"], s["table"], free, s["taken"], page,
+                                                         num, B, taken_out=s["taken"])
+        api.page_write(k, v, slots, s["kc"], s["vc"])
+        api.page_bounds(s["kc"], s["table"], s["cached"], lens, s["lo"], s["hi"])
+        picked = api.page_select(q, s["lo"], s["hi"], s["table"], lens, page, 3)
+        o = api.page_attend(q, s["kc"], s["vc"], s["table"], lens)
+        sparse = api.page_attend(q, s["kc"], s["vc"], s["table"], lens, picked=picked)
+        s["cached"].copy_(lens)
+        return lens, slots, picked, o, sparse
+
+    warm = start(state())
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(warm)
+    torch.cuda.synchronize()
+    a, b = start(state()), start(state())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step(a)
+    start(a)
+    a["cached"].copy_(ints([0, 15, 16, 100, 0]))
+    a["taken"].copy_(ints([10]))
+    for i in range(40):
+        for t, seed in ((q, 1), (k, 2), (v, 3)):
+            t.copy_(torch.randn(t.shape, generator=torch.Generator(device="cuda").manual_seed(100 * i + seed), device="cuda"))
+        graph.replay()
+        want = step(b)
+        for x, y in zip(captured, want):
+            assert torch.equal(x, y), i
+        for name in a:
+            assert torch.equal(a[name], b[name]), (i, name)
+    assert a["cached"].tolist() == [40, 55, 56, 140, 0]
+    wo, _, to, _ = P.attend(q, a["kc"], a["vc"], a["table"], a["cached"], dtype="bf16")
+    assert ((P.f64(captured[3]) - wo).abs() <= to).all()
+
+
+# ---- With the value path ----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_serving_steps(api, dtype):
+    """A prefill step and decode steps as a server runs them: v from value_routed,
+    page_map, page_write, page_bounds, then attention over all pages and over
+    selected ones; the cache's content and both outputs against plain ones."""
+    d, E, n, kv, G, page, num = 256, 8, 512, 4, 4, 16, 60
+    io = P.IO[dtype]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    rnd = lambda *shape: torch.randn(*shape, generator=g, device="cuda")
+    Wr, br, Wv = 0.1 * rnd(E, d), 0.01 * rnd(E), (rnd(E, n, d) / 16).to(io)
+    Wq, Wk = rnd(kv * G * 128, d) / 16, rnd(kv * 128, d) / 16
+    kc, vc = (torch.full((num, kv, page, 128), math.nan).to(io).to(P.CACHE[dtype]).cuda() for _ in range(2))
+    lo, hi = (torch.zeros(num, kv, 128).to(io).to(P.CACHE[dtype]).cuda() for _ in range(2))
+    ks = vs = None
+    if dtype == "e4m3":
+        ks, vs = 0.02 + 0.01 * torch.rand(kv, device="cuda"), 0.01 + 0.01 * torch.rand(kv, device="cuda")
+    table = torch.full((4, 14), -1, dtype=I32, device="cuda")
+    free, taken = torch.randperm(num, generator=g, device="cuda").to(I32), ints([0])
+    cached = ints([0, 0, 0, 0])
+    history = [[], [], [], []]
+    for step, added in enumerate([[50, 1, 0, 130], [1, 1, 17, 1], [1, 1, 1, 1], [1, 1, 1, 1], [0, 1, 0, 1]]):
+        T = sum(added) + 2
+        x = rnd(T, d).to(io)
+        q = (x.float() @ Wq.T).to(io).view(T, kv * G, 128)
+        k = (x.float() @ Wk.T).to(io).view(T, kv, 128)
+        v = api.value_routed(x, Wr, br, Wv, 2)
+        lens, starts, slots, positions, taken = api.page_map(cached, ints(added), table, free, taken, page, num, T)
+        ok(api)
+        api.page_write(k, v, slots, kc, vc, ks, vs)
+        ok(api)
+        api.page_bounds(kc, table, cached, lens, lo, hi)
+        ok(api)
+        at = 0
+        for b, a in enumerate(added):
+            assert positions[at:at + a].tolist() == list(range(len(history[b]), len(history[b]) + a))
+            history[b] += [(k[at + i].cpu(), v[at + i].view(kv, 128).cpu()) for i in range(a)]
+            at += a
+        assert slots[at:].tolist() == [-1, -1]
+        for b in range(4):  # what the cache holds is what was written
+            for i, (kk, vv) in enumerate(history[b]):
+                at_k = kc[table[b, i // page].item(), :, i % page].cpu()
+                at_v = vc[table[b, i // page].item(), :, i % page].cpu()
+                if dtype == "e4m3":
+                    kk = (kk.float() / ks.cpu()[:, None]).clamp(-448, 448).to(kc.dtype)
+                    vv = (vv.float() / vs.cpu()[:, None]).clamp(-448, 448).to(vc.dtype)
+                assert torch.equal(at_k.float(), kk.float()) and torch.equal(at_v.float(), vv.float())
+        last = (starts[1:] - 1).clamp(min=0).long()
+        s = dict(q=q[last].contiguous(), k=kc, v=vc, ks=ks, vs=vs, table=table, lens=lens)
+        check_attend(api, s, dtype)
+        picked = api.page_select(s["q"], lo, hi, table, lens, page, 3)
+        ok(api)
+        assert torch.equal(picked.cpu(), P.select(s["q"], lo, hi, table, lens, page, 3))
+        check_attend(api, s, dtype, picked=picked)
+        cached = lens
+    assert taken.item() == sum(P.ceil_div(len(h), page) for h in history)
