@@ -469,94 +469,115 @@ def value_attend_host(x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, Wv: t
 
 _CACHE_IO = {torch.float32: torch.float32, torch.bfloat16: torch.bfloat16, torch.float8_e4m3fn: torch.bfloat16}
 _STATUS_BYTES = 256
+_I32 = torch.int32
+_RSQRT_128 = 0.08838834764831845
 
 
-def _on(dev: torch.device, **tensors) -> None:
-    """Every tensor on `dev`: the library sees addresses only."""
+def _on(index: int, **tensors) -> None:
+    """Every tensor on CUDA device `index`: the library sees addresses only."""
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
 def _elsewhere(t: torch.Tensor) -> bool:
     """Whether t's device is not the current one (whose stream a call uses)."""
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("the paged calls take CUDA tensors")
-    return t.device.index != torch.cuda.current_device()
+    return index != torch.cuda.current_device()
 
 
-def _vector(t: torch.Tensor, name: str, n: int, dtype=torch.int32) -> None:
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+def _vector(t: torch.Tensor, name: str, n: int, dtype=_I32) -> None:
+    if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} vector of {n}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _row_stride(t: torch.Tensor, name: str, width: int) -> int:
     """Elements from one row to the next of a tensor whose rows (all dims but
     the first) hold `width` elements in order."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3 and strides[1:] == (shape[2], 1) and shape[1] * shape[2] == width <= strides[0] and shape[0] > 1:
+        return strides[0]
     want = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size != 1 and stride != want:
+    for size, stride in zip(shape[:0:-1], strides[:0:-1]):
+        if stride != want and size != 1:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
         want *= size
     if want != width:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected rows of {width} elements")
-    if t.shape[0] <= 1:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected rows of {width} elements")
+    if shape[0] <= 1:
         return width
-    if t.stride(0) < width:
+    if strides[0] < width:
         raise ValueError(f"{name}: rows overlap")
-    return t.stride(0)
+    return strides[0]
 
 
-def _heads(t: torch.Tensor, name: str, dtype) -> None:
-    if t.dtype != dtype:
+def _heads(t: torch.Tensor, name: str, dtype):
+    """(rows, heads) of a (rows, heads, 128) tensor."""
+    shape = t.shape
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.dim() != 3 or t.shape[2] != 128:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected (rows, heads, 128)")
+    if len(shape) != 3 or shape[2] != 128:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected (rows, heads, 128)")
+    return shape[0], shape[1]
 
 
-def _pages(dev, k_cache, v_cache=None, k_scale=None, v_scale=None):
-    """The mova_pages of a cache, and its shape (num_pages, KV heads, page_size)."""
-    dtype, strides = k_cache.dtype, [0, 0]
+def _pages(index: int, k_cache, v_cache=None, k_scale=None, v_scale=None):
+    """The mova_pages of a cache, and its (num_pages, KV heads)."""
+    dtype, shape = k_cache.dtype, k_cache.shape
     if dtype not in _CACHE_IO:
         raise ValueError(f"k_cache: dtype {dtype} not in {tuple(_CACHE_IO)}")
-    if k_cache.dim() != 4 or k_cache.shape[3] != 128:
-        raise ValueError(f"k_cache: shape {tuple(k_cache.shape)}, expected (num_pages, KV heads, page_size, 128)")
-    num, kv, page, _ = k_cache.shape
-    for i, (name, t) in enumerate((("k_cache", k_cache), ("v_cache", v_cache))):
-        if t is None:
-            continue
-        if t.dtype != dtype or t.shape != k_cache.shape:
-            raise ValueError(f"{name}: expected {dtype} of shape {tuple(k_cache.shape)}")
-        strides[i] = _row_stride(t, name, kv * page * 128)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is not None:
-            if dtype != torch.float8_e4m3fn:
-                raise ValueError(f"{name}: only float8_e4m3fn caches have scales")
-            _vector(t, name, kv, torch.float32)
-    _on(dev, k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    p = _lib.Pages(k_cache.data_ptr(), 0 if v_cache is None else v_cache.data_ptr(), _DT[dtype], num, kv, page,
-                   strides[0], strides[1], 0 if k_scale is None else k_scale.data_ptr(),
-                   0 if v_scale is None else v_scale.data_ptr())
-    return p, num, kv, page
+    if len(shape) != 4 or shape[3] != 128:
+        raise ValueError(f"k_cache: shape {tuple(shape)}, expected (num_pages, KV heads, page_size, 128)")
+    num, kv, page, _ = shape
+    k_stride = 0 if k_cache.is_contiguous() else _row_stride(k_cache, "k_cache", kv * page * 128)
+    v, v_stride = 0, 0
+    if v_cache is not None:
+        if v_cache.dtype is not dtype or v_cache.shape != shape:
+            raise ValueError(f"v_cache: expected {dtype} of shape {tuple(shape)}")
+        v_stride = 0 if v_cache.is_contiguous() else _row_stride(v_cache, "v_cache", kv * page * 128)
+        v = v_cache.data_ptr()
+    ks = vs = 0
+    if k_scale is not None or v_scale is not None:
+        if dtype is not torch.float8_e4m3fn:
+            raise ValueError("k_scale, v_scale: only float8_e4m3fn caches have scales")
+        if k_scale is not None:
+            _vector(k_scale, "k_scale", kv, torch.float32)
+            ks = k_scale.data_ptr()
+        if v_scale is not None:
+            _vector(v_scale, "v_scale", kv, torch.float32)
+            vs = v_scale.data_ptr()
+        _on(index, k_scale=k_scale, v_scale=v_scale)
+    if k_cache.get_device() != index or (v_cache is not None and v_cache.get_device() != index):
+        _on(index, k_cache=k_cache, v_cache=v_cache)
+    return _lib.Pages(k_cache.data_ptr(), v, _DT[dtype], num, kv, page, k_stride, v_stride, ks, vs), num, kv
 
 
-def _table(dev, table, lens, B: int):
+def _table(index: int, table, lens, B: int):
     """(row stride, max_pages) of a page table for B requests."""
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != B:
-        raise ValueError(f"table: expected int32 of shape ({B}, max_pages), got {table.dtype} {tuple(table.shape)}")
+    shape = table.shape
+    if table.dtype is not _I32 or len(shape) != 2 or shape[0] != B:
+        raise ValueError(f"table: expected int32 of shape ({B}, max_pages), got {table.dtype} {tuple(shape)}")
     _vector(lens, "lens", B)
-    _on(dev, table=table, lens=lens)
-    return _row_stride(table, "table", table.shape[1]), table.shape[1]
+    if table.get_device() != index or lens.get_device() != index:
+        _on(index, table=table, lens=lens)
+    return (shape[1] if table.is_contiguous() else _row_stride(table, "table", shape[1])), shape[1]
 
 
 def _page_ws(ws, nbytes: int, dev):
+    """(address, bytes, stream handle): `ws`, or the current stream's workspace."""
+    handle = _current_stream_handle()
     if ws is None:
-        ws = _workspace(nbytes, dev)
-    else:
-        _on(dev, ws=ws)
-        if not ws.is_contiguous():
-            raise ValueError("ws must be contiguous")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+        own = _WS.get((dev, handle))
+        ws = own.buf if own is not None else None
+        if ws is None or ws.numel() < nbytes:
+            ws = _workspace(nbytes, dev)
+        return ws.data_ptr(), ws.numel(), handle
+    _on(dev.index, ws=ws)
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), handle
 
 
 @functools.lru_cache(maxsize=256)
@@ -577,24 +598,24 @@ def page_map(cached: torch.Tensor, added: torch.Tensor, table: torch.Tensor, fre
     if _elsewhere(cached):
         with torch.cuda.device(cached.device):
             return page_map(cached, added, table, free_pages, taken, page_size, num_pages, tokens, taken_out, ws)
-    dev, B = cached.device, cached.shape[0]
-    _vector(cached, "cached", B)
+    dev, index, B, n_free = cached.device, cached.get_device(), cached.shape[0], free_pages.shape[0]
+    stride, max_pages = _table(index, table, cached, B)
     _vector(added, "added", B)
-    _vector(free_pages, "free_pages", free_pages.shape[0])
+    _vector(free_pages, "free_pages", n_free)
     _vector(taken, "taken", 1)
-    stride, max_pages = _table(dev, table, cached, B)
-    lens, starts, slots, positions, out = torch.empty(2 * B + 2 + 2 * tokens, dtype=torch.int32, device=dev).split(
+    if added.get_device() != index or free_pages.get_device() != index or taken.get_device() != index:
+        _on(index, added=added, free_pages=free_pages, taken=taken)
+    lens, starts, slots, positions, out = torch.empty(2 * (B + tokens + 1), dtype=_I32, device=dev).split_with_sizes(
         [B, B + 1, tokens, tokens, 1])
     if taken_out is not None:
         _vector(taken_out, "taken_out", 1)
+        _on(index, taken_out=taken_out)
         out = taken_out
-    _on(dev, added=added, free_pages=free_pages, taken=taken, taken_out=taken_out)
-    p_ws, n_ws = _page_ws(ws, _STATUS_BYTES, dev)
+    p_ws, n_ws, stream = _page_ws(ws, _STATUS_BYTES, dev)
     _lib.check(_lib.load().mova_page_map(
-        cached.data_ptr(), added.data_ptr(), B, table.data_ptr(), stride, max_pages, free_pages.data_ptr(),
-        free_pages.shape[0], taken.data_ptr(), page_size, num_pages, tokens, lens.data_ptr(), starts.data_ptr(),
-        slots.data_ptr(), positions.data_ptr(), out.data_ptr(), p_ws, n_ws, _current_stream_handle()),
-        "mova_page_map")
+        cached.data_ptr(), added.data_ptr(), B, table.data_ptr(), stride, max_pages, free_pages.data_ptr(), n_free,
+        taken.data_ptr(), page_size, num_pages, tokens, lens.data_ptr(), starts.data_ptr(), slots.data_ptr(),
+        positions.data_ptr(), out.data_ptr(), p_ws, n_ws, stream), "mova_page_map")
     return lens, starts, slots, positions, out
 
 
@@ -607,28 +628,29 @@ def page_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: t
     if _elsewhere(k):
         with torch.cuda.device(k.device):
             return page_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, ws)
-    dev, T = k.device, k.shape[0]
-    p, _, kv, _ = _pages(dev, k_cache, v_cache, k_scale, v_scale)
+    dev, index, T = k.device, k.get_device(), k.shape[0]
+    p, _, kv = _pages(index, k_cache, v_cache, k_scale, v_scale)
     io = _CACHE_IO[k_cache.dtype]
-    if k.dtype != io or v.dtype != io:
+    if k.dtype is not io or v.dtype is not io:
         raise ValueError(f"k, v: {k.dtype}, {v.dtype}; a {k_cache.dtype} cache takes {io}")
     k_stride, v_stride = _row_stride(k, "k", kv * 128), _row_stride(v, "v", kv * 128)
     if v.shape[0] != T:
         raise ValueError(f"v: {v.shape[0]} tokens, expected {T}")
     _vector(slots, "slots", T)
-    _on(dev, v=v, slots=slots)
-    p_ws, n_ws = _page_ws(ws, _STATUS_BYTES, dev)
+    if v.get_device() != index or slots.get_device() != index:
+        _on(index, v=v, slots=slots)
+    p_ws, n_ws, stream = _page_ws(ws, _STATUS_BYTES, dev)
     _lib.check(_lib.load().mova_page_write(k.data_ptr(), v.data_ptr(), _DT[io], k_stride, v_stride, slots.data_ptr(),
-                                           T, ctypes.addressof(p), p_ws, n_ws, _current_stream_handle()),
-               "mova_page_write")
+                                           T, ctypes.addressof(p), p_ws, n_ws, stream), "mova_page_write")
 
 
-def _bounds(dev, k_lo, k_hi, num: int, kv: int, dtype) -> None:
-    for name, t in (("k_lo", k_lo), ("k_hi", k_hi)):
-        if t.dtype != dtype or t.shape != (num, kv, 128) or not t.is_contiguous():
-            raise ValueError(f"{name}: expected contiguous {dtype} of shape {(num, kv, 128)}, got {t.dtype} "
+def _bounds(index: int, k_lo, k_hi, want, dtype) -> None:
+    for t in (k_lo, k_hi):
+        if t.dtype is not dtype or t.shape != want or not t.is_contiguous():
+            raise ValueError(f"k_lo, k_hi: expected contiguous {dtype} of shape {tuple(want)}, got {t.dtype} "
                              f"{tuple(t.shape)}")
-    _on(dev, k_lo=k_lo, k_hi=k_hi)
+        if t.get_device() != index:
+            _on(index, k_lo=k_lo, k_hi=k_hi)
 
 
 def page_bounds(k_cache: torch.Tensor, table: torch.Tensor, cached: torch.Tensor, lens: torch.Tensor,
@@ -639,16 +661,17 @@ def page_bounds(k_cache: torch.Tensor, table: torch.Tensor, cached: torch.Tensor
     if _elsewhere(k_cache):
         with torch.cuda.device(k_cache.device):
             return page_bounds(k_cache, table, cached, lens, k_lo, k_hi, ws)
-    dev, B = k_cache.device, lens.shape[0]
-    p, num, kv, _ = _pages(dev, k_cache)
-    stride, max_pages = _table(dev, table, lens, B)
+    dev, index, B = k_cache.device, k_cache.get_device(), lens.shape[0]
+    p, num, kv = _pages(index, k_cache)
+    stride, max_pages = _table(index, table, lens, B)
     _vector(cached, "cached", B)
-    _on(dev, cached=cached)
-    _bounds(dev, k_lo, k_hi, num, kv, k_cache.dtype)
-    p_ws, n_ws = _page_ws(ws, _STATUS_BYTES, dev)
+    if cached.get_device() != index:
+        _on(index, cached=cached)
+    _bounds(index, k_lo, k_hi, (num, kv, 128), k_cache.dtype)
+    p_ws, n_ws, stream = _page_ws(ws, _STATUS_BYTES, dev)
     _lib.check(_lib.load().mova_page_bounds(ctypes.addressof(p), table.data_ptr(), stride, max_pages,
                                             cached.data_ptr(), lens.data_ptr(), B, k_lo.data_ptr(), k_hi.data_ptr(),
-                                            p_ws, n_ws, _current_stream_handle()), "mova_page_bounds")
+                                            p_ws, n_ws, stream), "mova_page_bounds")
 
 
 def page_select(q: torch.Tensor, k_lo: torch.Tensor, k_hi: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -659,23 +682,21 @@ def page_select(q: torch.Tensor, k_lo: torch.Tensor, k_hi: torch.Tensor, table: 
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return page_select(q, k_lo, k_hi, table, lens, page_size, top, ws)
-    dev = q.device
-    if k_lo.dtype not in _CACHE_IO or k_lo.dim() != 3:
-        raise ValueError(f"k_lo: expected (num_pages, KV heads, 128) of a cache's dtype, got {k_lo.dtype} "
-                         f"{tuple(k_lo.shape)}")
-    num, kv, _ = k_lo.shape
-    _bounds(dev, k_lo, k_hi, num, kv, k_lo.dtype)
-    _heads(q, "q", _CACHE_IO[k_lo.dtype])
-    B, H, _ = q.shape
+    dev, index, dtype, shape = q.device, q.get_device(), k_lo.dtype, k_lo.shape
+    if dtype not in _CACHE_IO or len(shape) != 3 or shape[2] != 128:
+        raise ValueError(f"k_lo: expected (num_pages, KV heads, 128) of a cache's dtype, got {dtype} {tuple(shape)}")
+    num, kv, _ = shape
+    _bounds(index, k_lo, k_hi, shape, dtype)
+    B, H = _heads(q, "q", _CACHE_IO[dtype])
     q_stride = _row_stride(q, "q", H * 128)
-    stride, max_pages = _table(dev, table, lens, B)
-    picked = torch.empty((B, kv, top), dtype=torch.int32, device=dev)
-    p = _lib.Pages(0, 0, _DT[k_lo.dtype], num, kv, page_size, 0, 0, 0, 0)
-    p_ws, n_ws = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
+    stride, max_pages = _table(index, table, lens, B)
+    picked = torch.empty(B, kv, top, dtype=_I32, device=dev)
+    p = _lib.Pages(0, 0, _DT[dtype], num, kv, page_size, 0, 0, 0, 0)
+    p_ws, n_ws, stream = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
     _lib.check(_lib.load().mova_page_select(q.data_ptr(), _DT[q.dtype], q_stride, H, ctypes.addressof(p),
                                             k_lo.data_ptr(), k_hi.data_ptr(), table.data_ptr(), stride, max_pages,
-                                            lens.data_ptr(), B, top, picked.data_ptr(), p_ws, n_ws,
-                                            _current_stream_handle()), "mova_page_select")
+                                            lens.data_ptr(), B, top, picked.data_ptr(), p_ws, n_ws, stream),
+               "mova_page_select")
     return picked
 
 
@@ -690,31 +711,31 @@ def page_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, t
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return page_attend(q, k_cache, v_cache, table, lens, scale, picked, k_scale, v_scale, return_lse, out, ws)
-    dev = q.device
-    p, _, kv, _ = _pages(dev, k_cache, v_cache, k_scale, v_scale)
-    _heads(q, "q", _CACHE_IO[k_cache.dtype])
-    B, H, _ = q.shape
+    dev, index = q.device, q.get_device()
+    p, _, kv = _pages(index, k_cache, v_cache, k_scale, v_scale)
+    B, H = _heads(q, "q", _CACHE_IO[k_cache.dtype])
     q_stride = _row_stride(q, "q", H * 128)
-    stride, max_pages = _table(dev, table, lens, B)
+    stride, max_pages = _table(index, table, lens, B)
     p_picked = top = 0
     if picked is not None:
-        if picked.dtype != torch.int32 or picked.dim() != 3 or picked.shape[:2] != (B, kv) or not picked.is_contiguous():
+        if picked.dtype is not _I32 or picked.dim() != 3 or picked.shape[:2] != (B, kv) or not picked.is_contiguous():
             raise ValueError(f"picked: expected contiguous int32 of shape ({B}, {kv}, top), got {picked.dtype} "
                              f"{tuple(picked.shape)}")
-        _on(dev, picked=picked)
+        if picked.get_device() != index:
+            _on(index, picked=picked)
         p_picked, top = picked.data_ptr(), picked.shape[2]
     if out is None:
-        out = torch.empty((B, H, 128), dtype=q.dtype, device=dev)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_contiguous():
+        out = torch.empty(B, H, 128, dtype=q.dtype, device=dev)
+    elif out.dtype is not q.dtype or out.shape != q.shape or not out.is_contiguous():
         raise ValueError(f"out: expected contiguous {q.dtype} of shape {tuple(q.shape)}")
     else:
-        _on(dev, out=out)
-    lse = torch.empty((B, H), dtype=torch.float32, device=dev) if return_lse else None
-    p_ws, n_ws = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
+        _on(index, out=out)
+    lse = torch.empty(B, H, dtype=torch.float32, device=dev) if return_lse else None
+    p_ws, n_ws, stream = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
     _lib.check(_lib.load().mova_page_attend(
         q.data_ptr(), _DT[q.dtype], q_stride, H, ctypes.addressof(p), table.data_ptr(), stride, max_pages,
-        lens.data_ptr(), B, 0.08838834764831845 if scale is None else scale, p_picked, top, out.data_ptr(),
-        lse.data_ptr() if return_lse else None, p_ws, n_ws, _current_stream_handle()), "mova_page_attend")
+        lens.data_ptr(), B, _RSQRT_128 if scale is None else scale, p_picked, top, out.data_ptr(),
+        lse.data_ptr() if return_lse else None, p_ws, n_ws, stream), "mova_page_attend")
     return (out, lse) if return_lse else out
 
 

@@ -50,7 +50,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kPadDim = kHeadDim + 4;  // merge rows, padded against bank conflicts
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -428,13 +427,15 @@ __device__ __forceinline__ int worker_of(int u, int W, int U) {
   return static_cast<int>((static_cast<long long>(u + 1) * W - 1) / U);
 }
 
-// Dynamic shared memory: the ring, the merge rows of kWarps x G heads, the
-// fp32 queries, and the prefix.
-template <int M>
-__host__ __device__ constexpr size_t attend_smem(int G, int B) {
-  return kRingBytes + static_cast<size_t>(kWarps) * G * kPadDim * 4 + (M == kF32 ? kMaxGroup * kHeadDim * 4 : 0) +
-         static_cast<size_t>(B + 1) * 4;
+// Dynamic shared memory: the ring, the fp32 queries (NT heads), the prefix.
+template <int M, int NT>
+__host__ __device__ constexpr size_t attend_smem(int B) {
+  return kRingBytes + (M == kF32 ? NT * kHeadDim * 4 : 0) + static_cast<size_t>(B + 1) * 4;
 }
+
+// Where the warps are joined, head's dimension d lies at d ^ join_swizzle(head):
+// the four heads that a warp stores at once then use different banks.
+__device__ __forceinline__ int join_swizzle(int head) { return ((head >> 1) & 3) << 3; }
 
 // NT: mma column tiles of 8 heads, or fp32 heads.
 template <int M, int NT>
@@ -453,9 +454,8 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = s.G, kv = s.a.kv, B = s.a.B, shift = s.a.shift;
-  float* merge = reinterpret_cast<float*>(smem + kRingBytes);
-  float* q_sm = merge + kWarps * G * kPadDim;
-  int* pre = reinterpret_cast<int*>(q_sm + (M == kF32 ? kMaxGroup * kHeadDim : 0));
+  float* q_sm = reinterpret_cast<float*>(smem + kRingBytes);
+  int* pre = reinterpret_cast<int*>(q_sm + (M == kF32 ? NT * kHeadDim : 0));
   const int w = blockIdx.x;
 
   if (tid == 0) sm_bad = kNoBad;
@@ -586,8 +586,14 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
       }
       const bool row_end = t + 1 == tiles;
       if (row_end || i + 1 == count) {
-        // Join the four warps: maxima, sums and outputs through shared memory.
+        // Join the four warps: maxima, sums and outputs through shared memory.  A
+        // warp's outputs (at most 16 heads x 512 bytes) go where the tile it has
+        // just used was: the next copies into that stage are started after this.
         const int g = lane >> 2, t4 = lane & 3;
+        const int join0 = stage * kStageBytes / 4;
+        float* join = reinterpret_cast<float*>(smem) + join0;  // warp x's at x * kStages * kStageBytes / 4
+        constexpr int kJoinWarp = kStages * kStageBytes / 4;
+        __syncwarp();  // every lane has read the tile
         if constexpr (M == kF32) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
             for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             if (n < G) {
               if (lane == 0) sm_m[warp][n] = st.m[n][0], sm_l[warp][n] = l;
-              *reinterpret_cast<float4*>(&merge[(warp * G + n) * kPadDim + 4 * lane]) =
+              *reinterpret_cast<float4*>(&join[warp * kJoinWarp + n * kHeadDim + ((4 * lane) ^ join_swizzle(n))]) =
                   make_float4(st.o[0][n][0], st.o[0][n][1], st.o[0][n][2], st.o[0][n][3]);
             }
           }
@@ -611,11 +617,16 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
               const int head = n * 8 + 2 * t4 + c;
               if (head < G) {
                 if (g == 0) sm_m[warp][head] = st.m[n][c], sm_l[warp][head] = l;
-                float* row = &merge[(warp * G + head) * kPadDim];
+                float* row = &join[warp * kJoinWarp + head * kHeadDim];
+                const int swz = join_swizzle(head);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                  row[16 * x + (M == kE8 ? 2 * g : g)] = st.o[x][n][c];
-                  row[16 * x + (M == kE8 ? 2 * g + 1 : g + 8)] = st.o[x][n][c + 2];
+                  if constexpr (M == kE8) {
+                    *reinterpret_cast<float2*>(&row[(16 * x + 2 * g) ^ swz]) = make_float2(st.o[x][n][c], st.o[x][n][c + 2]);
+                  } else {
+                    row[(16 * x + g) ^ swz] = st.o[x][n][c];
+                    row[(16 * x + g + 8) ^ swz] = st.o[x][n][c + 2];
+                  }
                 }
               }
             }
@@ -633,7 +644,7 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
           for (int x = 0; x < kWarps; ++x) {
             const float f = ex2(sm_m[x][head] - ref_of(m));
             l = fmaf(sm_l[x][head], f, l);
-            o = fmaf(merge[(x * G + head) * kPadDim + tid], f, o);
+            o = fmaf(join[x * kJoinWarp + head * kHeadDim + (tid ^ join_swizzle(head))], f, o);
           }
           o *= v_scale;
           if (done) {
@@ -731,9 +742,9 @@ template <int M, int NT>
 cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
   auto kern = page_attend_kernel<M, NT>;
   static bool done[64] = {false};
-  cudaError_t err = allow_smem(kern, attend_smem<M>(kMaxGroup, kMaxRequests), done);
+  cudaError_t err = allow_smem(kern, attend_smem<M, NT>(kMaxRequests), done);
   if (err != cudaSuccess) return err;
-  const size_t smem = attend_smem<M>(s.G, s.a.B);
+  const size_t smem = attend_smem<M, NT>(s.a.B);
   const int per_sm = 2 * (smem + 2048) <= 227 * 1024 ? 2 : 1;
   const long long most = static_cast<long long>(s.a.B) * s.a.kv *
                          (((static_cast<long long>(s.a.max_pages) << s.a.shift) + kWarps * Tile<M>::keys - 1) /

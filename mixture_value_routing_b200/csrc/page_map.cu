@@ -21,24 +21,26 @@ namespace mova {
 
 namespace {
 
-constexpr int kMapThreads = 1024;
 constexpr int kMapMaxCluster = 8;
 // Tokens per CTA at which another CTA joins: four per thread.
 constexpr int kMapTokensPerCta = 4096;
 
-__global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapArgs a) {
+// kCluster: a cluster of several CTAs; otherwise one CTA, launched without one.
+template <int kThreads, bool kCluster>
+__global__ void __launch_bounds__(kThreads) page_map_kernel(const MapArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) char smem[];
   __shared__ int sm_bad, sm_used;
   long long* starts = reinterpret_cast<long long*>(smem);
   long long* pre = starts + a.B + 1;
   int* cached = reinterpret_cast<int*>(pre + a.B + 1);
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, rank = static_cast<int>(cluster.block_rank());
-  const int CTAs = static_cast<int>(cluster.num_blocks());
+  int* added = cached + a.B;
+  const int tid = threadIdx.x;
+  const int rank = kCluster ? static_cast<int>(blockIdx.x) : 0, CTAs = kCluster ? static_cast<int>(gridDim.x) : 1;
   const int page_size = 1 << a.shift;
   if (tid == 0) sm_bad = kNoBad, sm_used = 0;
-  cluster.sync();  // rank 0's sm_bad is set before another CTA reduces into it
+  // Rank 0's sm_bad is set before another CTA reduces into it.
+  if constexpr (kCluster) cg::this_cluster().sync();
   pdl_wait();
   pdl_trigger();
   const int taken = a.taken[0];
@@ -48,32 +50,30 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapArgs a) 
   auto pages = [&](long long tokens) { return (tokens + page_size - 1) >> a.shift; };
   auto fits = [&](int c, int n) { return c >= 0 && n >= 0 && static_cast<long long>(c) + n <= cap; };
 
-  request_scan<kMapThreads>(a.B, starts, [&](int b) {
-    cached[b] = a.cached[b];
-    const int n = a.added[b];
-    return static_cast<long long>(n < 0 ? 0 : n);
-  });
-  request_scan<kMapThreads>(a.B, pre, [&](int b) {
-    const int c = cached[b], n = a.added[b];
-    return fits(c, n) ? pages(static_cast<long long>(c) + n) - pages(c) : 0LL;
+  request_scan2<kThreads>(a.B, starts, pre, [&](int b, long long& tokens, long long& need) {
+    const int c = a.cached[b], n = a.added[b];
+    cached[b] = c;
+    added[b] = n;
+    tokens = n < 0 ? 0 : n;
+    need = fits(c, n) ? pages(static_cast<long long>(c) + n) - pages(c) : 0LL;
   });
   // Whether request b gets its pages; its share of the free list is [pre[b], pre[b + 1]).
-  auto granted = [&](int b, int n) {
-    return fits(cached[b], n) && (pre[b + 1] == pre[b] || pre[b + 1] <= avail);
+  auto granted = [&](int b) {
+    return fits(cached[b], added[b]) && (pre[b + 1] == pre[b] || pre[b + 1] <= avail);
   };
-  for (int b = tid; b < a.B; b += kMapThreads) {
-    const int c = cached[b], n = a.added[b];
-    const bool ok = granted(b, n);
+  for (int b = tid; b < a.B; b += kThreads) {
+    const bool ok = granted(b);
     if (!ok || starts[b + 1] > a.T) atomicMin(&sm_bad, b);
-    if (pre[b + 1] <= avail) atomicMax(&sm_used, static_cast<int>(pre[b + 1]));
-    if (rank == 0) a.lens[b] = ok ? c + n : (c < 0 ? 0 : c);
+    // The last request within the free pages: what is handed out.
+    if (pre[b + 1] <= avail && (b + 1 == a.B || pre[b + 2] > avail)) sm_used = static_cast<int>(pre[b + 1]);
+    if (rank == 0) a.lens[b] = ok ? cached[b] + added[b] : max(cached[b], 0);
   }
   if (rank == 0)
-    for (int b = tid; b <= a.B; b += kMapThreads)
+    for (int b = tid; b <= a.B; b += kThreads)
       a.starts[b] = static_cast<int>(starts[b] > 0x7fffffff ? 0x7fffffff : starts[b]);
   __syncthreads();
   const int used = sm_used;
-  const int all = CTAs * kMapThreads, me = rank * kMapThreads + tid;
+  const int all = CTAs * kThreads, me = rank * kThreads + tid;
   for (int x = me; x < used; x += all) {
     const int b = request_of(pre, a.B, static_cast<long long>(x));
     const long long j = pages(cached[b]) + x - pre[b];
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapArgs a) 
     if (i < total) {
       const int b = request_of(starts, a.B, i);
       const int c = cached[b];
-      if (granted(b, a.added[b])) {
+      if (granted(b)) {
         pos = static_cast<int>(c + i - starts[b]);
         const int j = pos >> a.shift, have = static_cast<int>(pages(c));
         const int page = j < have ? a.table[b * a.table_stride + j] : a.free_pages[taken + pre[b] + j - have];
@@ -99,8 +99,11 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapArgs a) 
     a.positions[i] = pos;
   }
   __syncthreads();
-  if (rank != 0 && tid == 0) atomicMin(cluster.map_shared_rank(&sm_bad, 0), sm_bad);
-  cluster.sync();
+  if constexpr (kCluster) {
+    cg::cluster_group cluster = cg::this_cluster();
+    if (rank != 0 && tid == 0) atomicMin(cluster.map_shared_rank(&sm_bad, 0), sm_bad);
+    cluster.sync();
+  }
   if (rank == 0 && tid == 0) {
     a.taken_out[0] = taken + used;
     a.sb->code = sm_bad == kNoBad ? MOVA_OK : MOVA_ERR_DEVICE_CHECK;
@@ -108,30 +111,37 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapArgs a) 
   }
 }
 
+template <int kThreads, bool kCluster>
+cudaError_t launch_map_t(const MapArgs& a, int ctas, cudaStream_t stream) {
+  static bool done[64] = {false};
+  auto kern = page_map_kernel<kThreads, kCluster>;
+  constexpr size_t kMost = (kMaxRequests + 1) * 16 + kMaxRequests * 8;
+  cudaError_t err = allow_smem(kern, kMost, done);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.B + 1) * 16 + static_cast<size_t>(a.B) * 8;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCluster ? 2 : 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
 }  // namespace
 
 cudaError_t launch_page_map(const MapArgs& a, cudaStream_t stream) {
-  static bool done[64] = {false};
-  constexpr size_t kMost = (kMaxRequests + 1) * 16 + kMaxRequests * 4;
-  cudaError_t err = allow_smem(page_map_kernel, kMost, done);
-  if (err != cudaSuccess) return err;
   int ctas = 1;
   while (ctas < kMapMaxCluster && a.T > ctas * kMapTokensPerCta) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kMapThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(a.B + 1) * 16 + static_cast<size_t>(a.B) * 4;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  note_launch();
-  return cudaLaunchKernelEx(&cfg, page_map_kernel, a);
+  if (ctas > 1) return launch_map_t<1024, true>(a, ctas, stream);
+  return a.B <= 256 && a.T <= 1024 ? launch_map_t<256, false>(a, 1, stream) : launch_map_t<1024, false>(a, 1, stream);
 }
 
 }  // namespace mova

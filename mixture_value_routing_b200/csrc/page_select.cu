@@ -36,22 +36,29 @@ constexpr int kBins = 1 << kDigit;
 
 using u64 = unsigned long long;
 
-__device__ __forceinline__ void load4(const float* p, double (&d)[4]) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, double (&d)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-  d[0] = a.x, d[1] = a.y, d[2] = b.x, d[3] = b.y;
-}
-__device__ __forceinline__ void load4(const uint8_t* p, double (&d)[4]) {
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
+// Four consecutive elements, as stored and in fp64.
+template <typename E> struct Four;
+template <> struct Four<float> {
+  using Raw = uint4;
+  static __device__ __forceinline__ void get(const Raw& u, double (&d)[4]) {
+    d[0] = __uint_as_float(u.x), d[1] = __uint_as_float(u.y), d[2] = __uint_as_float(u.z), d[3] = __uint_as_float(u.w);
+  }
+};
+template <> struct Four<__nv_bfloat16> {
+  using Raw = uint2;
+  static __device__ __forceinline__ void get(const Raw& u, double (&d)[4]) {
+    d[0] = __uint_as_float(u.x << 16), d[1] = __uint_as_float(u.x & 0xffff0000u);
+    d[2] = __uint_as_float(u.y << 16), d[3] = __uint_as_float(u.y & 0xffff0000u);
+  }
+};
+template <> struct Four<uint8_t> {
+  using Raw = uint32_t;
+  static __device__ __forceinline__ void get(const Raw& u, double (&d)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    d[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<uint8_t>(u >> (8 * i)), __NV_E4M3)));
-}
+    for (int i = 0; i < 4; ++i)
+      d[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<uint8_t>(u >> (8 * i)), __NV_E4M3)));
+  }
+};
 
 // An unsigned integer in the order of the scores; 0 is below all of them.
 __device__ __forceinline__ u64 sortable(double s) {
@@ -108,14 +115,15 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectA
       row = b * kv + h;
       pages = pages_of(s.a, b) - 1;
       const Q* src = static_cast<const Q*>(s.q) + b * s.q_stride + static_cast<long long>(h) * s.G * kHeadDim + 4 * lane;
+      typename Four<Q>::Raw raw[NH];
+#pragma unroll
+      for (int n = 0; n < NH; ++n)
+        raw[n] = *reinterpret_cast<const typename Four<Q>::Raw*>(src + (n < s.G ? n : 0) * kHeadDim);
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
-        if (n < s.G) {
-          load4(src + n * kHeadDim, q[n]);
-        } else {
+        Four<Q>::get(raw[n], q[n]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) q[n][i] = 0.0;
-        }
+        for (int i = 0; i < 4; ++i) q[n][i] = q[n][i] + 0.0;  // -0 counts as 0: its sign bit picks no bound
       }
     }
     const int page0 = (u - first) * kPages;
@@ -127,21 +135,27 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectA
         atomicMin(&sm_bad, b);
       }
     }
+    // All pages' bounds are on their way before the first is used; a page that
+    // is none reads page 0 and is dropped below.
+    typename Four<E>::Raw raw_lo[kPages], raw_hi[kPages];
+#pragma unroll
+    for (int p = 0; p < kPages; ++p) {
+      const int at = max(0, __shfl_sync(0xffffffffu, id, p));
+      const long long off = (static_cast<long long>(at) * kv + h) * kHeadDim + 4 * lane;
+      raw_lo[p] = *reinterpret_cast<const typename Four<E>::Raw*>(static_cast<const E*>(s.lo) + off);
+      raw_hi[p] = *reinterpret_cast<const typename Four<E>::Raw*>(static_cast<const E*>(s.hi) + off);
+    }
     double sum[32];
 #pragma unroll
     for (int p = 0; p < kPages; ++p) {
-      const int at = __shfl_sync(0xffffffffu, id, p);
-      double lo[4] = {0.0, 0.0, 0.0, 0.0}, hi[4] = {0.0, 0.0, 0.0, 0.0};
-      if (at >= 0) {
-        const long long off = (static_cast<long long>(at) * kv + h) * kHeadDim + 4 * lane;
-        load4(static_cast<const E*>(s.lo) + off, lo);
-        load4(static_cast<const E*>(s.hi) + off, hi);
-      }
+      double lo[4], hi[4];
+      Four<E>::get(raw_lo[p], lo);
+      Four<E>::get(raw_hi[p], hi);
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
         double x = 0.0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x = fma(q[n][i], q[n][i] < 0.0 ? lo[i] : hi[i], x);
+        for (int i = 0; i < 4; ++i) x = fma(q[n][i], __double2hiint(q[n][i]) < 0 ? lo[i] : hi[i], x);
         sum[p * NH + n] = x;
       }
     }
@@ -178,10 +192,8 @@ __device__ __forceinline__ u64 warp_min(u64 x) {
   return x;
 }
 
-// Exclusive prefix sum of x over the CTA; *all receives the total.  One
-// barrier before and after, so calls may follow one another.
-__device__ __forceinline__ int cta_scan(int x, int* all) {
-  __shared__ int sums[kTopThreads / 32];
+// Exclusive prefix sum of x over the CTA.  `sums` is the caller's alone.
+__device__ __forceinline__ int cta_scan(int x, int (&sums)[kTopThreads / 32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = x;
 #pragma unroll
@@ -189,22 +201,41 @@ __device__ __forceinline__ int cta_scan(int x, int* all) {
     const int up = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += up;
   }
-  __syncthreads();
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  int before = 0, total = 0;
+  int before = 0;
 #pragma unroll
-  for (int w = 0; w < kTopThreads / 32; ++w) {
+  for (int w = 0; w < kTopThreads / 32; ++w)
     if (w < warp) before += sums[w];
-    total += sums[w];
-  }
-  *all = total;
   return before + incl - x;
 }
+
+// The keys of one (request, KV head): thread t holds keys t + i * kTopThreads,
+// the first kHeld of them in registers, the rest (long requests) in memory.
+constexpr int kHeld = 16;
+struct Keys {
+  const u64* from;
+  int N;
+  u64 held[kHeld];
+  __device__ __forceinline__ Keys(const u64* p, int n) : from(p), N(n) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const int at = threadIdx.x + i * kTopThreads;
+      held[i] = at < N ? from[at] : 0ULL;
+    }
+  }
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (static_cast<int>(threadIdx.x) + i * kTopThreads < N) f(held[i]);
+    for (int at = threadIdx.x + kHeld * kTopThreads; at < N; at += kTopThreads) f(from[at]);
+  }
+};
 
 __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs s, int score_ctas, StatusBlock* sb) {
   __shared__ int hist[kBins];
   __shared__ u64 sm_min[kTopThreads / 32], sm_max[kTopThreads / 32];
+  __shared__ int sums[kTopThreads / 32], sums2[kTopThreads / 32];
   __shared__ int sm_bin, sm_above, sm_in;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
@@ -228,18 +259,17 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   if (tid == 0) out[top - 1] = n - 1;
   if (top == 1) return;
   const int N = n - 1;
-  const u64* keys = s.keys + static_cast<long long>(blockIdx.x) * s.a.max_pages;
+  const Keys keys(s.keys + static_cast<long long>(blockIdx.x) * s.a.max_pages, N);
 
   u64 least = ~0ULL, most_inv = ~0ULL;  // the greatest, as the least complement
-#pragma unroll 4
-  for (int i = tid; i < N; i += kTopThreads) {
-    const u64 k = keys[i];
+  keys.each([&](u64 k) {
     least = k < least ? k : least;
     most_inv = ~k < most_inv ? ~k : most_inv;
-  }
+  });
   least = warp_min(least);
   most_inv = warp_min(most_inv);
   if (lane == 0) sm_min[warp] = least, sm_max[warp] = most_inv;
+  for (int i = tid; i < kBins; i += kTopThreads) hist[i] = 0;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kTopThreads / 32; ++w) {
@@ -253,27 +283,24 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   bool all = false;    // every one of them
   while (bits > 0 && !all) {
     const int width = bits < kDigit ? bits : kDigit, sh = bits - width;
-    for (int i = tid; i < kBins; i += kTopThreads) hist[i] = 0;
-    __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < N; i += kTopThreads) {
-      const u64 k = keys[i];
+    keys.each([&](u64 k) {
       if (bits == 64 || (k >> bits) == prefix) atomicAdd(&hist[static_cast<int>(k >> sh) & ((1 << width) - 1)], 1);
-    }
+    });
     __syncthreads();
     // Thread i holds the bins below kBins - 4 i, from the top.
     constexpr int kPer = kBins / kTopThreads;
-    int c[kPer], mine = 0, total;
+    int c[kPer], mine = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       c[j] = hist[kBins - 1 - (tid * kPer + j)];
       mine += c[j];
     }
-    int above = cta_scan(mine, &total);
+    int above = cta_scan(mine, sums);  // its barrier: every bin has been read
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (above < need && need <= above + c[j]) sm_bin = kBins - 1 - (tid * kPer + j), sm_above = above, sm_in = c[j];
       above += c[j];
+      hist[kBins - 1 - (tid * kPer + j)] = 0;  // for the next digit
     }
     __syncthreads();
     prefix = (prefix << width) | static_cast<u64>(sm_bin);
@@ -282,24 +309,33 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     bits = sh;
     __syncthreads();
   }
-  // Each thread a contiguous run of pages: counts, one scan, and out.
-  const int run = (N + kTopThreads - 1) / kTopThreads;
-  const int i0 = min(N, tid * run), i1 = min(N, i0 + run);
-  int more = 0, same = 0, total;
-  for (int i = i0; i < i1; ++i) {
-    const u64 k = bits == 64 ? 0ULL : keys[i] >> bits;
-    more += k > prefix;
-    same += k == prefix;
-  }
-  const int more0 = cta_scan(more, &total);
-  const int same0 = cta_scan(same, &total);
-  int at = more0, eq = same0;
-  for (int i = i0; i < i1; ++i) {
-    const u64 k = bits == 64 ? 0ULL : keys[i] >> bits;
-    const bool gt = k > prefix, take = gt || (k == prefix && (all || eq < need));
-    if (take) out[at + min(eq, need)] = i;
-    at += gt;
-    eq += k == prefix;
+  // Places, in page order: kTopThreads pages at a time.
+  int base_more = 0, base_same = 0;
+  for (int at0 = 0, i = 0; at0 < N; at0 += kTopThreads, ++i) {
+    const int at = at0 + tid;
+    u64 k = 0ULL;
+    if (i < kHeld) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j)
+        if (j == i) k = keys.held[j];
+    } else if (at < N) {
+      k = keys.from[at];
+    }
+    k >>= bits;
+    const bool more = at < N && k > prefix, same = at < N && k == prefix;
+    const unsigned m = __ballot_sync(0xffffffffu, more), e = __ballot_sync(0xffffffffu, same);
+    const unsigned below = (1u << lane) - 1;
+    if (lane == 0) sums[warp] = __popc(m), sums2[warp] = __popc(e);
+    __syncthreads();
+    int more_at = base_more + __popc(m & below), same_at = base_same + __popc(e & below);
+#pragma unroll
+    for (int w = 0; w < kTopThreads / 32; ++w) {
+      const int x = sums[w], y = sums2[w];
+      if (w < warp) more_at += x, same_at += y;
+      base_more += x, base_same += y;
+    }
+    if (more || (same && (all || same_at < need))) out[more_at + min(same_at, need)] = at;
+    __syncthreads();
   }
 }
 

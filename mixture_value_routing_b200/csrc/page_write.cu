@@ -9,7 +9,8 @@
 //
 // page_bounds: lo / hi[page, h, d] = min / max over the page's keys, for pages
 // that the step filled: page_size * 128 elements read for 256 written, bound
-// by memory; one CTA per (page, head), all its loads in flight at once.
+// by memory.  A warp takes one (page, head) at a time, eight 512-byte loads in
+// flight, in packed 16-bit minima and maxima; nothing joins but its own lanes.
 #include <math.h>
 
 #include "paged.cuh"
@@ -121,52 +122,81 @@ cudaError_t launch_write_t(const void* k, const void* v, long long k_stride, lon
 
 // ---- Bounds --------------------------------------------------------------------
 
-constexpr int kBoundThreads = 256;
+constexpr int kBoundThreads = 128;
+constexpr int kBoundPerSm = 8;
 
-// Minimum and maximum that return NaN if either operand is NaN.
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
+// Least and greatest of packed elements, NaN if either operand is NaN.
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<uint32_t*>(&v); }
+__device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast<uint32_t*>(&v); }
+template <typename T> __device__ __forceinline__ T from_u32(uint32_t v) { return *reinterpret_cast<T*>(&v); }
 
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[4], float) {
-  f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
-}
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[8], __nv_bfloat16) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 x = __bfloat1622float2(h[i]);
-    f[2 * i] = x.x, f[2 * i + 1] = x.y;
+// Bounds of one 16-byte chunk of a key: kWords 32-bit words of packed fp32,
+// bf16 or (for E4M3, exactly) fp16.
+template <typename E> struct Range;
+template <> struct Range<float> {
+  static constexpr int kWords = 4;
+  static __device__ __forceinline__ void load(const uint4& u, uint32_t (&w)[4]) { w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w; }
+  static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return __float_as_uint(r);
   }
-}
-__device__ __forceinline__ void unpack(const uint4& u, float (&f)[16], uint8_t) {
-  const uint8_t* e = reinterpret_cast<const uint8_t*>(&u);
+  static __device__ __forceinline__ uint32_t greatest(uint32_t a, uint32_t b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+    return __float_as_uint(r);
+  }
+  static __device__ __forceinline__ uint4 store(const uint32_t (&w)[4]) { return make_uint4(w[0], w[1], w[2], w[3]); }
+};
+template <> struct Range<__nv_bfloat16> {
+  static constexpr int kWords = 4;
+  static __device__ __forceinline__ void load(const uint4& u, uint32_t (&w)[4]) { w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w; }
+  static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) {
+    return as_u32(__hmin2_nan(from_u32<__nv_bfloat162>(a), from_u32<__nv_bfloat162>(b)));
+  }
+  static __device__ __forceinline__ uint32_t greatest(uint32_t a, uint32_t b) {
+    return as_u32(__hmax2_nan(from_u32<__nv_bfloat162>(a), from_u32<__nv_bfloat162>(b)));
+  }
+  static __device__ __forceinline__ uint4 store(const uint32_t (&w)[4]) { return make_uint4(w[0], w[1], w[2], w[3]); }
+};
+template <> struct Range<uint8_t> {
+  static constexpr int kWords = 8;
+  static __device__ __forceinline__ void load(const uint4& u, uint32_t (&w)[8]) {
+    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) f[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(e[i], __NV_E4M3)));
-}
-__device__ __forceinline__ void put(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put(uint8_t* p, float v) { *p = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3); }
+    for (int i = 0; i < 8; ++i)
+      w[i] = as_u32(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(in[i >> 1] >> (16 * (i & 1))), __NV_E4M3)));
+  }
+  static __device__ __forceinline__ uint32_t least(uint32_t a, uint32_t b) {
+    return as_u32(__hmin2_nan(from_u32<__half2>(a), from_u32<__half2>(b)));
+  }
+  static __device__ __forceinline__ uint32_t greatest(uint32_t a, uint32_t b) {
+    return as_u32(__hmax2_nan(from_u32<__half2>(a), from_u32<__half2>(b)));
+  }
+  static __device__ __forceinline__ uint4 store(const uint32_t (&w)[8]) {
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(from_u32<__half2_raw>(w[2 * i]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(from_u32<__half2_raw>(w[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+      out[i] = lo | (hi << 16);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+  }
+};
 
 template <typename E>
 __global__ void __launch_bounds__(kBoundThreads)
 page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __restrict__ lo, E* __restrict__ hi,
                    StatusBlock* sb) {
+  using R = Range<E>;
   constexpr int kPer = 16 / sizeof(E);
-  constexpr int kCols = kHeadDim / kPer;            // 16-byte chunks of a key
-  constexpr int kRows = kBoundThreads / kCols;      // keys of one pass
+  constexpr int kCols = kHeadDim / kPer;  // 16-byte chunks of a key
+  constexpr int kRows = 32 / kCols;       // keys of one warp-wide load
+  constexpr int kLoads = 16 / kRows < 8 ? 16 / kRows : 8;  // in flight at once; pages have at least 16 keys
   extern __shared__ int pre[];
-  __shared__ float red[2][kBoundThreads / 32][kHeadDim];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool checks = blockIdx.x == gridDim.x - 1;
   __shared__ int bad;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) bad = kNoBad;
   pdl_wait();
   pdl_trigger();
@@ -186,7 +216,8 @@ page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __re
     *b = request_of(pre, a.B, item);
     return a.table[*b * a.table_stride + first_page(*b) + item - pre[*b]];
   };
-  if (checks) {
+  if (blockIdx.x == gridDim.x - 1) {
+    // The last CTA only looks the pages over and writes the status.
     for (int i = tid; i < items; i += kBoundThreads) {
       int b;
       const int page = page_of(i, &b);
@@ -199,46 +230,50 @@ page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __re
     }
     return;
   }
-  const int col = tid % kCols, row0 = tid / kCols;
+  const int col = lane % kCols, row0 = lane / kCols;
   const long long work = static_cast<long long>(items) * a.kv;
-  for (long long x = blockIdx.x; x < work; x += gridDim.x - 1) {
-    int b;
-    const int item = static_cast<int>(x / a.kv), h = static_cast<int>(x - static_cast<long long>(item) * a.kv);
-    const int page = page_of(item, &b);
-    if (page < 0 || page >= a.num_pages) continue;  // the same for the whole CTA
-    const E* src = static_cast<const E*>(a.k) + page * a.k_stride + (static_cast<long long>(h) << a.shift) * kHeadDim;
-    float l[kPer], u[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) l[i] = INFINITY, u[i] = -INFINITY;
-#pragma unroll 4
-    for (int r = row0; r < (1 << a.shift); r += kRows) {
-      float f[kPer];
-      unpack(*reinterpret_cast<const uint4*>(src + r * kHeadDim + col * kPer), f, E());
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) l[i] = min_nan(l[i], f[i]), u[i] = max_nan(u[i], f[i]);
+  const int W = (gridDim.x - 1) * (kBoundThreads / 32), w = blockIdx.x * (kBoundThreads / 32) + warp;
+  const long long x0 = w * work / W, x1 = (w + 1) * work / W;
+  int t_page = -1;  // page of (item, head) x0 + 32 n + lane
+  for (long long x = x0; x < x1; ++x) {
+    const int at = static_cast<int>(x - x0) & 31;
+    if (at == 0) {
+      int b;
+      t_page = x + lane < x1 ? page_of(static_cast<int>((x + lane) / a.kv), &b) : -1;
     }
-    // The rows of a warp, then the warps.
+    const int page = __shfl_sync(0xffffffffu, t_page, at);
+    if (page < 0 || page >= a.num_pages) continue;  // the same for the whole warp
+    const int h = static_cast<int>(x % a.kv);
+    const E* src = static_cast<const E*>(a.k) + page * a.k_stride + (static_cast<long long>(h) << a.shift) * kHeadDim +
+                   row0 * kHeadDim + col * kPer;
+    uint32_t l[R::kWords], u[R::kWords];
+    for (int r = 0; r < (1 << a.shift); r += kRows * kLoads) {
+      uint4 raw[kLoads];
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + (r + i * kRows) * kHeadDim);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        uint32_t v[R::kWords];
+        R::load(raw[i], v);
+#pragma unroll
+        for (int j = 0; j < R::kWords; ++j) {
+          l[j] = i == 0 && r == 0 ? v[j] : R::least(l[j], v[j]);
+          u[j] = i == 0 && r == 0 ? v[j] : R::greatest(u[j], v[j]);
+        }
+      }
+    }
 #pragma unroll
     for (int o = kCols; o < 32; o <<= 1)
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        l[i] = min_nan(l[i], __shfl_xor_sync(0xffffffffu, l[i], o));
-        u[i] = max_nan(u[i], __shfl_xor_sync(0xffffffffu, u[i], o));
+      for (int j = 0; j < R::kWords; ++j) {
+        l[j] = R::least(l[j], __shfl_xor_sync(0xffffffffu, l[j], o));
+        u[j] = R::greatest(u[j], __shfl_xor_sync(0xffffffffu, u[j], o));
       }
     if (lane < kCols) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) red[0][warp][lane * kPer + i] = l[i], red[1][warp][lane * kPer + i] = u[i];
+      const long long out = (static_cast<long long>(page) * a.kv + h) * kHeadDim + col * kPer;
+      *reinterpret_cast<uint4*>(lo + out) = R::store(l);
+      *reinterpret_cast<uint4*>(hi + out) = R::store(u);
     }
-    __syncthreads();
-    {
-      const int which = tid >> 7, d = tid & (kHeadDim - 1);
-      float m = red[which][0][d];
-#pragma unroll
-      for (int y = 1; y < kBoundThreads / 32; ++y)
-        m = which ? max_nan(m, red[1][y][d]) : min_nan(m, red[0][y][d]);
-      put((which ? hi : lo) + (static_cast<long long>(page) * a.kv + h) * kHeadDim + d, m);
-    }
-    __syncthreads();
   }
 }
 
@@ -246,7 +281,7 @@ template <typename E>
 cudaError_t launch_bounds_t(const PageArgs& a, const int32_t* cached, void* lo, void* hi, StatusBlock* sb,
                             cudaStream_t stream) {
   const long long most = static_cast<long long>(a.B) * a.max_pages * a.kv;
-  const long long grid = sm_count() * 6LL;  // 256 threads, 8 KB: six CTAs keep an SM's loads in flight
+  const long long grid = static_cast<long long>(sm_count()) * kBoundPerSm;
   return launch_pdl(page_bounds_kernel<E>, dim3(static_cast<unsigned>((most < grid ? most : grid) + 1)),
                     dim3(kBoundThreads), static_cast<size_t>(a.B + 1) * 4, stream, a, cached, static_cast<E*>(lo),
                     static_cast<E*>(hi), sb);

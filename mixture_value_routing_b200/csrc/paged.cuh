@@ -76,6 +76,38 @@ __device__ __forceinline__ void request_scan(int B, T* pre, F count) {
   __syncthreads();
 }
 
+// As request_scan, of two counts per request at once.
+template <int kThreads, typename F>
+__device__ __forceinline__ void request_scan2(int B, long long* pre1, long long* pre2, F count) {
+  __shared__ long long warp_sum[2][kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long carry1 = 0, carry2 = 0;
+  for (int base = 0; base < B; base += kThreads) {
+    const int b = base + tid;
+    long long c1 = 0, c2 = 0;
+    if (b < B) count(b, c1, c2);
+    long long i1 = c1, i2 = c2;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u1 = __shfl_up_sync(0xffffffffu, i1, o), u2 = __shfl_up_sync(0xffffffffu, i2, o);
+      if (lane >= o) i1 += u1, i2 += u2;
+    }
+    if (lane == 31) warp_sum[0][warp] = i1, warp_sum[1][warp] = i2;
+    __syncthreads();
+    long long before1 = carry1, before2 = carry2;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const long long s1 = warp_sum[0][w], s2 = warp_sum[1][w];
+      if (w < warp) before1 += s1, before2 += s2;
+      carry1 += s1, carry2 += s2;
+    }
+    if (b < B) pre1[b] = before1 + i1 - c1, pre2[b] = before2 + i2 - c2;
+    __syncthreads();
+  }
+  if (tid == 0) pre1[B] = carry1, pre2[B] = carry2;
+  __syncthreads();
+}
+
 // The last b in [0, B) with pre[b] <= x (pre[0] = 0 <= x < pre[B]).
 template <typename T>
 __device__ __forceinline__ int request_of(const T* pre, int B, T x) {

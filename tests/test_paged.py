@@ -202,9 +202,8 @@ def host(monkeypatch):
             return call
 
     monkeypatch.setattr(api, "_elsewhere", lambda t: False)
-    monkeypatch.setattr(api, "_page_ws", lambda ws, n, dev: (0, 0))
+    monkeypatch.setattr(api, "_page_ws", lambda ws, n, dev: (0, 0, 0))
     monkeypatch.setattr(api, "page_workspace_size", lambda *a: 0)
-    monkeypatch.setattr(api, "_current_stream_handle", lambda: 0)
     monkeypatch.setattr(api._lib, "load", Lib)
     return Reached
 
