@@ -43,6 +43,12 @@ except AttributeError:  # pragma: no cover - older torch
     _raw_stream = None
 
 
+try:
+    _current_device = torch._C._cuda_getDevice  # torch.cuda.current_device without its lazy initialisation
+except AttributeError:  # pragma: no cover - a torch built without CUDA
+    _current_device = torch.cuda.current_device
+
+
 def _current_stream_handle() -> int:
     """The handle of the current stream of the current device."""
     if _raw_stream is not None:
@@ -485,7 +491,7 @@ def _elsewhere(t: torch.Tensor) -> bool:
     index = t.get_device()
     if index < 0:
         raise ValueError("the paged calls take CUDA tensors")
-    return index != torch.cuda.current_device()
+    return index != _current_device()
 
 
 def _vector(t: torch.Tensor, name: str, n: int, dtype=_I32) -> None:
@@ -566,8 +572,9 @@ def _table(index: int, table, lens, B: int):
 
 
 def _page_ws(ws, nbytes: int, dev):
-    """(address, bytes, stream handle): `ws`, or the current stream's workspace."""
-    handle = _current_stream_handle()
+    """(address, bytes, stream handle): `ws`, or the current stream's workspace
+    on `dev`, the current device."""
+    handle = _raw_stream(dev.index) if _raw_stream is not None else _current_stream_handle()
     if ws is None:
         own = _WS.get((dev, handle))
         ws = own.buf if own is not None else None

@@ -37,6 +37,7 @@
 // token, head and dimension.
 #include <math.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -47,18 +48,22 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kStages = 3;
-constexpr int kStageBytes = 8192;
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kStageBytes = 8192;  // K and V of one warp's tile
+constexpr int kRingAlign = 256;
+#ifndef ST_F32
+#define ST_F32 2
+#define ST_B16 3
+#define ST_E8 2
+#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 enum Mode { kF32 = 0, kB16 = 1, kE8 = 2 };
 
 template <int M> struct Tile;  // of one warp
-template <> struct Tile<kF32> { using E = float;         static constexpr int keys = 8;  static constexpr int groups = 1; };
-template <> struct Tile<kB16> { using E = __nv_bfloat16; static constexpr int keys = 16; static constexpr int groups = 1; };
-template <> struct Tile<kE8>  { using E = uint8_t;       static constexpr int keys = 32; static constexpr int groups = 2; };
+template <> struct Tile<kF32> { using E = float;         static constexpr int keys = 8;  static constexpr int groups = 1; static constexpr int stages = ST_F32; };
+template <> struct Tile<kB16> { using E = __nv_bfloat16; static constexpr int keys = 16; static constexpr int groups = 1; static constexpr int stages = ST_B16; };
+template <> struct Tile<kE8>  { using E = uint8_t;       static constexpr int keys = 32; static constexpr int groups = 2; static constexpr int stages = ST_E8; };
 
 struct AttendArgs {
   PageArgs a;
@@ -84,6 +89,9 @@ __device__ __forceinline__ int places_of(const AttendArgs& s, int len) {
 
 __device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -133,8 +141,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// 2^x for a score below the running maximum (x <= 0, or NaN).
-__device__ __forceinline__ float ex2(float x) { return exp2f(x); }
+// 2^x for x <= 0 (or NaN), relative error 2^-22; below 2^-126 it is 0.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // The maximum to subtract: 0 while nothing has been seen.
 __device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
@@ -206,27 +218,30 @@ __device__ __forceinline__ void load_query(Query<M, NT>& r, const __nv_bfloat16*
   }
 }
 
-// Softmax of 16 keys' scores (rows g, g + 8 of the fragment): updates the
+// Softmax of H x 16 keys' scores (rows g, g + 8 of each fragment): updates the
 // state, and returns P^T as the second product's column operand.
-template <int M, int NT>
-__device__ __forceinline__ void softmax16(State<M, NT>& st, float (&s)[NT][4], const Query<M, NT>& q, int valid,
-                                          int lane, uint32_t (&p)[NT][2], uint32_t (&plo)[NT][2]) {
+template <int M, int NT, int H>
+__device__ __forceinline__ void softmax(State<M, NT>& st, const float (&s)[H][NT][4], const Query<M, NT>& q,
+                                        const int (&valid)[H], int lane, uint32_t (&p)[H][NT][2],
+                                        uint32_t (&plo)[H][NT][2]) {
   const int g = lane >> 2;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float x[4];
-    x[0] = g < valid ? s[n][0] * q.f[n][0] : -INFINITY;
-    x[1] = g < valid ? s[n][1] * q.f[n][1] : -INFINITY;
-    x[2] = g + 8 < valid ? s[n][2] * q.f[n][0] : -INFINITY;
-    x[3] = g + 8 < valid ? s[n][3] * q.f[n][1] : -INFINITY;
-    float top[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+    float x[H][4], top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        x[h][c] = (c < 2 ? g : g + 8) < valid[h] ? s[h][n][c] * q.f[n][c & 1] : -INFINITY;
+        top[c & 1] = fmaxf(top[c & 1], x[h][c]);
+      }
+    }
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
       top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
     }
-    const bool up = top[0] > st.m[n][0] || top[1] > st.m[n][1];
-    if (__any_sync(0xffffffffu, up)) {
+    if (__any_sync(0xffffffffu, top[0] > st.m[n][0] || top[1] > st.m[n][1])) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float m = fmaxf(st.m[n][c], top[c]);
@@ -240,24 +255,28 @@ __device__ __forceinline__ void softmax16(State<M, NT>& st, float (&s)[NT][4], c
         }
       }
     }
+    const float ref[2] = {ref_of(st.m[n][0]), ref_of(st.m[n][1])};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) x[c] = ex2(x[c] - ref_of(st.m[n][c & 1]));
-    st.l[n][0] += x[0] + x[2];
-    st.l[n][1] += x[1] + x[3];
-    if constexpr (M == kB16) {
-      // hi: the upper 16 bits (p truncated); lo: the rest, kept above zero so that
-      // an infinite value's products with both have one sign.
-      float lo[4];
+    for (int h = 0; h < H; ++h) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        lo[c] = fmaxf(x[c] - __uint_as_float(__float_as_uint(x[c]) & 0xffff0000u), x[c] * 0x1p-24f);
-      p[n][0] = transpose8x8(__byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x7632));
-      p[n][1] = transpose8x8(__byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x7632));
-      plo[n][0] = transpose8x8(pack_bf16(lo[0], lo[1]));
-      plo[n][1] = transpose8x8(pack_bf16(lo[2], lo[3]));
-    } else {
-      p[n][0] = transpose8x8(pack_f16(x[0], x[1]));
-      p[n][1] = transpose8x8(pack_f16(x[2], x[3]));
+      for (int c = 0; c < 4; ++c) x[h][c] = ex2(x[h][c] - ref[c & 1]);
+      st.l[n][0] += x[h][0] + x[h][2];
+      st.l[n][1] += x[h][1] + x[h][3];
+      if constexpr (M == kB16) {
+        // hi: the upper 16 bits (p truncated); lo: the rest, kept above zero so that
+        // an infinite value's products with both have one sign.
+        float lo[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          lo[c] = fmaxf(x[h][c] - __uint_as_float(__float_as_uint(x[h][c]) & 0xffff0000u), x[h][c] * 0x1p-24f);
+        p[h][n][0] = transpose8x8(__byte_perm(__float_as_uint(x[h][0]), __float_as_uint(x[h][1]), 0x7632));
+        p[h][n][1] = transpose8x8(__byte_perm(__float_as_uint(x[h][2]), __float_as_uint(x[h][3]), 0x7632));
+        plo[h][n][0] = transpose8x8(pack_bf16(lo[0], lo[1]));
+        plo[h][n][1] = transpose8x8(pack_bf16(lo[2], lo[3]));
+      } else {
+        p[h][n][0] = transpose8x8(pack_f16(x[h][0], x[h][1]));
+        p[h][n][1] = transpose8x8(pack_f16(x[h][2], x[h][3]));
+      }
     }
   }
 }
@@ -273,11 +292,12 @@ __device__ __forceinline__ void tile_b16(State<kB16, NT>& st, const Query<kB16, 
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int c = 0; c < 4; ++c) s[0][n][c] = s[1][n][c] = 0.0f;
-  const uint32_t krow = kt + (r8 + (lane & 8)) * 256;
+  // Rows are 256-byte aligned, so the swizzled chunk is an exclusive or away.
+  const uint32_t krow = kt + (r8 + (lane & 8)) * 256 + (((lane >> 4) ^ r8) << 4);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     uint32_t a[4];
-    ldsm4(a, krow + (((2 * k + (lane >> 4)) ^ r8) << 4));
+    ldsm4(a, krow ^ (k << 5));
 #pragma unroll
     for (int n = 0; n < NT; ++n) mma16816<kB16>(s[k & 1][n], a[0], a[1], a[2], a[3], q.b[k][n][0], q.b[k][n][1]);
   }
@@ -285,17 +305,19 @@ __device__ __forceinline__ void tile_b16(State<kB16, NT>& st, const Query<kB16, 
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int c = 0; c < 4; ++c) s[0][n][c] += s[1][n][c];
-  uint32_t p[NT][2], plo[NT][2];
-  softmax16<kB16, NT>(st, s[0], q, valid, lane, p, plo);
-  const uint32_t vrow = vt + (r8 + ((lane >> 4) << 3)) * 256;
+  uint32_t p[1][NT][2], plo[1][NT][2];
+  const float (&sum)[1][NT][4] = reinterpret_cast<const float (&)[1][NT][4]>(s);
+  const int valids[1] = {valid};
+  softmax<kB16, NT, 1>(st, sum, q, valids, lane, p, plo);
+  const uint32_t vrow = vt + (r8 + ((lane >> 4) << 3)) * 256 + ((((lane >> 3) & 1) ^ r8) << 4);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t a[4];
-    ldsm4t(a, vrow + (((2 * i + ((lane >> 3) & 1)) ^ r8) << 4));
+    ldsm4t(a, vrow ^ (i << 5));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      mma16816<kB16>(st.o[i][n], a[0], a[1], a[2], a[3], p[n][0], p[n][1]);
-      mma16816<kB16>(st.o[i][n], a[0], a[1], a[2], a[3], plo[n][0], plo[n][1]);
+      mma16816<kB16>(st.o[i][n], a[0], a[1], a[2], a[3], p[0][n][0], p[0][n][1]);
+      mma16816<kB16>(st.o[i][n], a[0], a[1], a[2], a[3], plo[0][n][0], plo[0][n][1]);
     }
   }
 }
@@ -316,11 +338,11 @@ __device__ __forceinline__ void tile_e8(State<kE8, NT>& st, const Query<kE8, NT>
 #pragma unroll
     for (int c = 0; c < 4; ++c) s[0][n][c] = s[1][n][c] = 0.0f;
   // Matrices: rows 0-7, 8-15 (first 16 keys), 16-23, 24-31 (second), one chunk.
-  const uint32_t krow = kt + (r8 + ((lane >> 3) << 3)) * 128;
+  const uint32_t krow = kt + lane * 128 + (r8 << 4);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     uint32_t a[4];
-    ldsm4(a, krow + ((k ^ r8) << 4));
+    ldsm4(a, krow ^ (k << 4));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t a0 = e4m3_lo(a[2 * h]), a1 = e4m3_lo(a[2 * h + 1]);
@@ -329,34 +351,14 @@ __device__ __forceinline__ void tile_e8(State<kE8, NT>& st, const Query<kE8, NT>
       for (int n = 0; n < NT; ++n) mma16816<kE8>(s[h][n], a0, a1, a2, a3, q.b[k][n][0], q.b[k][n][1]);
     }
   }
-  uint32_t p[2][NT][2], none[NT][2];
-  softmax16<kE8, NT>(st, s[0], q, valid0, lane, p[0], none);
-  // The second half's maximum may rescale the first half's output: not yet
-  // added, so its probabilities are formed against the final maximum instead.
-  float before[NT][2];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) before[n][0] = st.m[n][0], before[n][1] = st.m[n][1];
-  softmax16<kE8, NT>(st, s[1], q, valid1, lane, p[1], none);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const bool moved = before[n][0] != st.m[n][0] || before[n][1] != st.m[n][1];
-    if (__any_sync(0xffffffffu, moved)) {
-      const int g = lane >> 2;
-      float x[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool in = (c < 2 ? g : g + 8) < valid0;
-        x[c] = in ? ex2(s[0][n][c] * q.f[n][c & 1] - ref_of(st.m[n][c & 1])) : 0.0f;
-      }
-      p[0][n][0] = transpose8x8(pack_f16(x[0], x[1]));
-      p[0][n][1] = transpose8x8(pack_f16(x[2], x[3]));
-    }
-  }
-  const uint32_t vrow = vt + (r8 + ((lane >> 3) << 3)) * 128;
+  uint32_t p[2][NT][2], none[2][NT][2];
+  const int valids[2] = {valid0, valid1};
+  softmax<kE8, NT, 2>(st, s, q, valids, lane, p, none);
+  const uint32_t vrow = vt + lane * 128 + (r8 << 4);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     uint32_t a[4];
-    ldsm4t(a, vrow + ((i ^ r8) << 4));
+    ldsm4t(a, vrow ^ (i << 4));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint32_t x = __byte_perm(a[2 * h], 0, 0x3120), y = __byte_perm(a[2 * h + 1], 0, 0x3120);
@@ -430,7 +432,7 @@ __device__ __forceinline__ int worker_of(int u, int W, int U) {
 // Dynamic shared memory: the ring, the fp32 queries (NT heads), the prefix.
 template <int M, int NT>
 __host__ __device__ constexpr size_t attend_smem(int B) {
-  return kRingBytes + (M == kF32 ? NT * kHeadDim * 4 : 0) + static_cast<size_t>(B + 1) * 4;
+  return kRingAlign + kWarps * Tile<M>::stages * kStageBytes + (M == kF32 ? NT * kHeadDim * 4 : 0) + static_cast<size_t>(B + 1) * 4;
 }
 
 // Where the warps are joined, head's dimension d lies at d ^ join_swizzle(head):
@@ -445,16 +447,19 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
   constexpr int kKeys = Tile<M>::keys;
   constexpr int kGroups = Tile<M>::groups;
   constexpr int kUnit = kWarps * kKeys;
+  constexpr int kStages = Tile<M>::stages;
   constexpr int kRow = kHeadDim * sizeof(E);      // bytes of a key
   constexpr int kChunks = kRow / 16;
-  extern __shared__ __align__(128) char smem[];
+  extern __shared__ char smem_raw[];
   __shared__ float sm_m[kWarps][kMaxGroup], sm_l[kWarps][kMaxGroup];
   __shared__ int sm_valid[kWarps][kStages][2];
   __shared__ int sm_bad;
 
+  // The ring's rows are aligned to their size (tile_b16, tile_e8 count on it).
+  char* smem = smem_raw + ((kRingAlign - (smem_u32(smem_raw) & (kRingAlign - 1))) & (kRingAlign - 1));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = s.G, kv = s.a.kv, B = s.a.B, shift = s.a.shift;
-  float* q_sm = reinterpret_cast<float*>(smem + kRingBytes);
+  float* q_sm = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
   int* pre = reinterpret_cast<int*>(q_sm + (M == kF32 ? NT * kHeadDim : 0));
   const int w = blockIdx.x;
 
@@ -514,6 +519,16 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
   const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
   const char* k_base = static_cast<const char*>(s.a.k);
   const char* v_base = static_cast<const char*>(s.a.v);
+  constexpr int kRowsPer = 32 / kChunks;               // rows of one warp-wide copy
+  constexpr int kCopies = kKeys / kGroups / kRowsPer;  // of K, and of V, per group
+  constexpr int kPeriod = M == kF32 ? 2 : 8 / kRowsPer;  // copies after which the swizzle repeats
+  const int lane_off = (lane / kChunks) * kRow + (lane % kChunks) * 16;
+  uint32_t swz[kPeriod];
+#pragma unroll
+  for (int x = 0; x < kPeriod; ++x) {
+    const int r = x * kRowsPer + lane / kChunks, c = lane % kChunks;
+    swz[x] = r * kRow + ((M == kF32 ? c ^ ((r & 1) << 2) : c ^ (r & 7)) << 4);
+  }
   // Starts the copies of tile i (of this warp) into its stage.
   auto issue = [&](int i) {
     if ((i & 31) == 0) look_up(i);
@@ -528,19 +543,23 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
         const char* ks = k_base + (page * s.a.k_stride + row * kHeadDim) * static_cast<long long>(sizeof(E));
         const char* vs = v_base + (page * s.a.v_stride + row * kHeadDim) * static_cast<long long>(sizeof(E));
         if (lane == 0) sm_valid[warp][stage][j] = valid;
-        constexpr int kRowsPer = 32 / kChunks;  // rows of one warp-wide copy
-        constexpr int kCopies = kKeys / kGroups / kRowsPer;
-        const int c = lane % kChunks;
+        const uint32_t to = dst + j * 16 * kRow;
+        if (valid >= kKeys / kGroups) {
 #pragma unroll
-        for (int x = 0; x < kCopies; ++x) {
-          const int r = x * kRowsPer + lane / kChunks;  // within the group
-          const int rr = r + 16 * j;
-          const int swz = M == kF32 ? (c ^ ((rr & 1) << 2)) : (c ^ (rr & 7));
-          const uint32_t at = dst + rr * kRow + (swz << 4);
-          const int bytes = r < valid ? 16 : 0;
-          const long long off = r < valid ? static_cast<long long>(r) * kRow + c * 16 : 0;
-          cp16_zfill(at, ks + off, bytes);
-          cp16_zfill(at + kStageBytes / 2, vs + off, bytes);
+          for (int x = 0; x < kCopies; ++x) {
+            const uint32_t at = to + swz[x % kPeriod] + (x / kPeriod) * (kPeriod * kRowsPer * kRow);
+            cp16(at, ks + lane_off + x * kRowsPer * kRow);
+            cp16(at + kStageBytes / 2, vs + lane_off + x * kRowsPer * kRow);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < kCopies; ++x) {
+            const bool in = x * kRowsPer + lane / kChunks < valid;
+            const uint32_t at = to + swz[x % kPeriod] + (x / kPeriod) * (kPeriod * kRowsPer * kRow);
+            const int off = in ? lane_off + x * kRowsPer * kRow : 0;
+            cp16_zfill(at, ks + off, in ? 16 : 0);
+            cp16_zfill(at + kStageBytes / 2, vs + off, in ? 16 : 0);
+          }
         }
       }
     }
@@ -677,64 +696,99 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
 
 // Joins the partial results of each (request, KV head) that several workers
 // share, in the order of its keys; writes zeros where there is no token; and
-// the status.
-template <int M>
-__global__ void __launch_bounds__(kThreads) page_join_kernel(const AttendArgs s, int workers, StatusBlock* sb) {
+// the status.  kSplit groups of 128 threads (a dimension each) take every
+// kSplit-th eight parts, whose maxima, sums and outputs are loaded at once.
+template <int M, int kSplit>
+__global__ void __launch_bounds__(kHeadDim * kSplit)
+page_join_kernel(const AttendArgs s, int workers, StatusBlock* sb) {
   using Out = typename std::conditional<M == kF32, float, __nv_bfloat16>::type;
-  __shared__ float factor[kMaxWorkers];
-  __shared__ float red[kThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kAhead = 8;
+  __shared__ float sm_m[kSplit], sm_l[kSplit], sm_o[kSplit][kHeadDim];
+  const int tid = threadIdx.x & (kHeadDim - 1), group = threadIdx.x / kHeadDim;
   const int G = s.G, kv = s.a.kv, B = s.a.B;
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
+  const int b = blockIdx.x / kv, h = blockIdx.x - b * kv;
+  const int p0 = s.prefix[b], tiles = s.prefix[b + 1] - p0, U = kv * s.prefix[B];
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
     int bad = kNoBad;
-    for (int i = lane; i < workers; i += 32) bad = min(bad, s.bad[i]);
+    for (int i = threadIdx.x; i < workers; i += 32) bad = min(bad, s.bad[i]);
     bad = __reduce_min_sync(0xffffffffu, bad);
-    if (lane == 0) {
+    if (threadIdx.x == 0) {
       sb->code = bad == kNoBad ? MOVA_OK : MOVA_ERR_DEVICE_CHECK;
       sb->detail = bad == kNoBad ? 0 : bad;
     }
   }
-  const int b = blockIdx.x / kv, h = blockIdx.x - b * kv;
-  const int p0 = s.prefix[b], tiles = s.prefix[b + 1] - p0, U = kv * s.prefix[B];
   const int W = min(workers, U);
   const int first = blockIdx.y, step = gridDim.y;
   const long long at0 = static_cast<long long>(blockIdx.x) * G;
   Out* o = static_cast<Out*>(s.o);
   if (tiles == 0) {
     for (int head = first; head < G; head += step) {
-      o[(at0 + head) * kHeadDim + tid] = from_f32<Out>(0.0f);
-      if (s.lse != nullptr && tid == 0) s.lse[at0 + head] = -INFINITY;
+      if (group == 0) o[(at0 + head) * kHeadDim + tid] = from_f32<Out>(0.0f);
+      if (s.lse != nullptr && threadIdx.x == 0) s.lse[at0 + head] = -INFINITY;
     }
     return;
   }
   const int u0 = kv * p0 + h * tiles;
   const int w0 = worker_of(u0, W, U), parts = worker_of(u0 + tiles - 1, W, U) - w0 + 1;
   if (parts == 1) return;
-  const size_t size = static_cast<size_t>(G) * (kHeadDim + 2);
+  const int size = G * (kHeadDim + 2);
   // Worker w0 begins this row (its second place), the others continue it.
-  auto part = [&](int i) { return s.part + (static_cast<size_t>(w0 + i) * 2 + (i == 0 ? 1 : 0)) * size; };
+  const float* part0 = s.part + static_cast<size_t>(w0) * 2 * size;
   for (int head = first; head < G; head += step) {
-    float m = -INFINITY;
-    for (int i = tid; i < parts; i += kThreads) m = fmaxf(m, part(i)[G * kHeadDim + head]);
+    float m = -INFINITY, l = 0.0f, acc = 0.0f;
+    for (int i0 = group * kAhead; i0 < parts; i0 += kSplit * kAhead) {
+      float pm[kAhead], pl[kAhead], po[kAhead];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    if (lane == 0) red[warp] = m;
-    __syncthreads();
+      for (int x = 0; x < kAhead; ++x) {
+        const int i = min(i0 + x, parts - 1);
+        const float* part = part0 + (2 * i + (i == 0 ? 1 : 0)) * size;
+        pm[x] = part[G * kHeadDim + head];
+        pl[x] = part[G * (kHeadDim + 1) + head];
+        po[x] = part[head * kHeadDim + tid];
+      }
+      float top = m;
 #pragma unroll
-    for (int x = 0; x < kThreads / 32; ++x) m = fmaxf(m, red[x]);
-    for (int i = tid; i < parts; i += kThreads) factor[i] = ex2(part(i)[G * kHeadDim + head] - ref_of(m));
-    __syncthreads();
-    float l = 0.0f, acc = 0.0f;
-#pragma unroll 8
-    for (int i = 0; i < parts; ++i) {
-      l = fmaf(part(i)[G * (kHeadDim + 1) + head], factor[i], l);
-      acc = fmaf(part(i)[head * kHeadDim + tid], factor[i], acc);
+      for (int x = 0; x < kAhead; ++x) top = fmaxf(top, pm[x]);
+      const float a = ex2(m - ref_of(top));
+      m = top;
+      l *= a;
+      acc *= a;
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        if (i0 + x < parts) {
+          const float f = ex2(pm[x] - ref_of(m));
+          l = fmaf(pl[x], f, l);
+          acc = fmaf(po[x], f, acc);
+        }
+      }
     }
-    o[(at0 + head) * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : acc / l);
-    if (s.lse != nullptr && tid == 0) s.lse[at0 + head] = (m + log2f(l)) * kLn2;
-    __syncthreads();
+    if constexpr (kSplit > 1) {
+      if (tid == 0) sm_m[group] = m, sm_l[group] = l;
+      sm_o[group][tid] = acc;
+      __syncthreads();
+      if (group == 0) {
+        float top = m;
+#pragma unroll
+        for (int x = 1; x < kSplit; ++x) top = fmaxf(top, sm_m[x]);
+        const float a = ex2(m - ref_of(top));
+        l *= a;
+        acc *= a;
+#pragma unroll
+        for (int x = 1; x < kSplit; ++x) {
+          const float f = ex2(sm_m[x] - ref_of(top));
+          l = fmaf(sm_l[x], f, l);
+          acc = fmaf(sm_o[x][tid], f, acc);
+        }
+        m = top;
+      }
+    }
+    if (group == 0) {
+      o[(at0 + head) * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : acc / l);
+      if (s.lse != nullptr && tid == 0) s.lse[at0 + head] = (m + log2f(l)) * kLn2;
+    }
+    if constexpr (kSplit > 1) __syncthreads();
   }
 }
 
@@ -745,7 +799,7 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   cudaError_t err = allow_smem(kern, attend_smem<M, NT>(kMaxRequests), done);
   if (err != cudaSuccess) return err;
   const size_t smem = attend_smem<M, NT>(s.a.B);
-  const int per_sm = 2 * (smem + 2048) <= 227 * 1024 ? 2 : 1;
+  const int per_sm = static_cast<int>(std::min<size_t>(3, (227 * 1024) / (smem + 2048)));
   const long long most = static_cast<long long>(s.a.B) * s.a.kv *
                          (((static_cast<long long>(s.a.max_pages) << s.a.shift) + kWarps * Tile<M>::keys - 1) /
                           (kWarps * Tile<M>::keys));
@@ -754,9 +808,14 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   if (W > most) W = most < 1 ? 1 : most;
   err = launch_pdl(kern, dim3(static_cast<unsigned>(W)), dim3(kThreads), smem, stream, s);
   if (err != cudaSuccess) return err;
+  // A CTA per query head while they all fit at once; few rows can have many
+  // parts each, so those get four groups of threads.
   const int rows = s.a.B * s.a.kv;
-  return launch_pdl(page_join_kernel<M>, dim3(rows, rows * s.G <= 4096 ? s.G : 1), dim3(kThreads), 0, stream, s,
-                    static_cast<int>(W), sb);
+  const bool few = static_cast<long long>(rows) * s.G <= sm_count();
+  if (few)
+    return launch_pdl(page_join_kernel<M, 4>, dim3(rows, s.G), dim3(4 * kHeadDim), 0, stream, s, static_cast<int>(W), sb);
+  return launch_pdl(page_join_kernel<M, 1>, dim3(rows, static_cast<long long>(rows) * s.G <= 4096 ? s.G : 1),
+                    dim3(kHeadDim), 0, stream, s, static_cast<int>(W), sb);
 }
 
 }  // namespace

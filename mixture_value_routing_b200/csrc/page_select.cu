@@ -6,14 +6,14 @@
 // and, of the request's full pages, the `top - 1` greatest (ties: the lower
 // page number), with the last page always, in ascending order.
 //
-// Scores: a warp takes 32 / NH pages at a time (NH heads, padded to 4, 8 or
-// 16); a lane holds 4 dimensions of the queries in fp64 and accumulates one
-// sum per (page, head), 32 of them, which 31 exchanges reduce and spread over
-// the lanes at once.  fp64 because neighbouring scores decide what is read:
-// with fp32 sums the choice would depend on their order.  2 x 128 elements
-// are read for 128 G fp64 FMAs, a ratio at which the fp64 pipes and memory
-// are about level for G = 4.  Scores are stored as unsigned integers in the
-// same order (NaN greatest, -0 = +0).
+// Scores: the formula is q+ . hi + q- . lo with q split by sign, a product of
+// (heads) x (2 * 128) by (2 * 128) x (pages).  A warp takes 8 pages at a time
+// and forms it with fp64 matrix instructions (m8n8k4): 8 heads by 8 pages, the
+// pages' bounds as loaded, 16 bytes a lane, whose dimensions q's registers
+// match.  fp64 because neighbouring scores decide what is read: with fp32 sums
+// the choice would depend on their order.  Products of the parts are exact for
+// bf16 and E4M3 bounds.  Scores are stored as unsigned integers in the same
+// order (NaN greatest, -0 = +0).
 //
 // Selection: one CTA per (request, KV head) finds the K-th greatest score by
 // radix search: the digits start below the bits that the least and the
@@ -29,31 +29,29 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScorePerSm = 4;
+constexpr int kScorePerSm = 2;
+constexpr int kPages = 8;  // of one batch
 constexpr int kTopThreads = 512;
 constexpr int kDigit = 11;
 constexpr int kBins = 1 << kDigit;
 
 using u64 = unsigned long long;
 
-// Four consecutive elements, as stored and in fp64.
-template <typename E> struct Four;
-template <> struct Four<float> {
-  using Raw = uint4;
-  static __device__ __forceinline__ void get(const Raw& u, double (&d)[4]) {
-    d[0] = __uint_as_float(u.x), d[1] = __uint_as_float(u.y), d[2] = __uint_as_float(u.z), d[3] = __uint_as_float(u.w);
+// One 32-bit word of stored elements in fp64.
+template <typename E> struct Word;
+template <> struct Word<float> {
+  static constexpr int kPer = 1;
+  static __device__ __forceinline__ void get(uint32_t u, double (&d)[1]) { d[0] = __uint_as_float(u); }
+};
+template <> struct Word<__nv_bfloat16> {
+  static constexpr int kPer = 2;
+  static __device__ __forceinline__ void get(uint32_t u, double (&d)[2]) {
+    d[0] = __uint_as_float(u << 16), d[1] = __uint_as_float(u & 0xffff0000u);
   }
 };
-template <> struct Four<__nv_bfloat16> {
-  using Raw = uint2;
-  static __device__ __forceinline__ void get(const Raw& u, double (&d)[4]) {
-    d[0] = __uint_as_float(u.x << 16), d[1] = __uint_as_float(u.x & 0xffff0000u);
-    d[2] = __uint_as_float(u.y << 16), d[3] = __uint_as_float(u.y & 0xffff0000u);
-  }
-};
-template <> struct Four<uint8_t> {
-  using Raw = uint32_t;
-  static __device__ __forceinline__ void get(const Raw& u, double (&d)[4]) {
+template <> struct Word<uint8_t> {
+  static constexpr int kPer = 4;
+  static __device__ __forceinline__ void get(uint32_t u, double (&d)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       d[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<uint8_t>(u >> (8 * i)), __NV_E4M3)));
@@ -79,18 +77,40 @@ struct SelectArgs {
   int32_t* picked;
 };
 
+__device__ __forceinline__ double value(float x) { return x; }
+__device__ __forceinline__ double value(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ double value(uint8_t x) { return __half2float(__half(__nv_cvt_fp8_to_halfraw(x, __NV_E4M3))); }
+
 __device__ __forceinline__ int pages_of(const PageArgs& a, int b) {
   const int len = clamp_len(a.lens[b], a.max_pages, a.shift);
   return (len + (1 << a.shift) - 1) >> a.shift;
 }
 
-template <typename Q, typename E, int NH>
-__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectArgs s) {
-  constexpr int kPages = 32 / NH;
+// c (8 heads x 8 pages) += a (8 heads x 4 dimensions) b (4 dimensions x 8 pages).
+__device__ __forceinline__ void mma884(double (&c)[2], double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0,%1}, {%2}, {%3}, {%0,%1};"
+               : "+d"(c[0]), "+d"(c[1]) : "d"(a), "d"(b));
+}
+
+// The dimensions of this lane (t = lane & 3) come in chunks of 16 stored bytes:
+// chunk i holds dimensions (t + 4 i) * kPer + {0 .. kPer - 1}.
+template <typename E> struct Chunk {
+  static constexpr int kPer = 16 / sizeof(E);
+  static constexpr int kCount = kHeadDim / kPer / 4;
+};
+
+// NT: tiles of 8 heads.  One tile's q stays in registers in fp64, split by
+// sign; two tiles' q stays as loaded and is converted for each batch of pages.
+template <typename Q, typename E, int NT>
+__global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const SelectArgs s) {
+  using C = Chunk<E>;
+  constexpr int kWords = C::kCount * 4;                       // 32-bit words of a lane's bounds
+  constexpr int kQWords = 32 / Word<Q>::kPer;                 // and of its 32 elements of q
+  constexpr int kQVec = kQWords / C::kCount / 4;              // 16-byte loads of q per chunk
   extern __shared__ int pre[];
   __shared__ int sm_bad;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int B = s.a.B, kv = s.a.kv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int B = s.a.B, kv = s.a.kv, G = s.G;
   if (tid == 0) sm_bad = kNoBad;
   pdl_wait();
   pdl_trigger();
@@ -104,80 +124,168 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const SelectA
   const int U = kv * pre[B], W = gridDim.x * kScoreWarps, w = blockIdx.x * kScoreWarps + warp;
   const int u0 = static_cast<int>(static_cast<long long>(w) * U / W);
   const int u1 = static_cast<int>(static_cast<long long>(w + 1) * U / W);
-  double q[NH][4];
-  int row = -1, b = 0, h = 0, tiles = 1, first = 0, pages = 0;
+
+  // Where a batch of pages lies: its request and KV head, and its first page.
+  struct At { int b, h, page0, pages; };
+  auto locate = [&](int u) {
+    At r;
+    r.b = request_of(pre, B, u / kv);
+    const int tiles = pre[r.b + 1] - pre[r.b], rem = u - kv * pre[r.b];
+    r.h = rem / tiles;
+    r.page0 = (rem - r.h * tiles) * kPages;
+    r.pages = pages_of(s.a, r.b) - 1;
+    return r;
+  };
+  // Page g of a batch as a page number, -1 if it is none.
+  auto look_up = [&](const At& r) {
+    if (r.page0 + g >= r.pages) return -1;
+    const int id = s.a.table[r.b * s.a.table_stride + r.page0 + g];
+    if (id >= 0 && id < s.a.num_pages) return id;
+    atomicMin(&sm_bad, r.b);
+    return -1;
+  };
+  // A page that is none reads page 0; its score is dropped.
+  auto load = [&](const At& r, int id, uint32_t (&lo)[kWords], uint32_t (&hi)[kWords]) {
+    const long long off = (static_cast<long long>(max(id, 0)) * kv + r.h) * kHeadDim + t * C::kPer;
+    const E* pl = static_cast<const E*>(s.lo) + off;
+    const E* ph = static_cast<const E*>(s.hi) + off;
+#pragma unroll
+    for (int i = 0; i < C::kCount; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(pl + i * 4 * C::kPer);
+      const uint4 y = *reinterpret_cast<const uint4*>(ph + i * 4 * C::kPer);
+      lo[4 * i] = x.x, lo[4 * i + 1] = x.y, lo[4 * i + 2] = x.z, lo[4 * i + 3] = x.w;
+      hi[4 * i] = y.x, hi[4 * i + 1] = y.y, hi[4 * i + 2] = y.z, hi[4 * i + 3] = y.w;
+    }
+  };
+
+  uint32_t q_raw[NT][kQWords];
+  double q_pos[NT == 1 ? 32 : 1], q_neg[NT == 1 ? 32 : 1];
+  uint32_t lo[kWords], hi[kWords];
+  At at{}, next{};
+  int id = -1, next_id = -1, row = -1;
+  if (u0 < u1) {
+    at = locate(u0);
+    id = look_up(at);
+    load(at, id, lo, hi);
+  }
   for (int u = u0; u < u1; ++u) {
-    if (row < 0 || u - first == tiles) {  // the next (request, KV head)
-      b = request_of(pre, B, u / kv);
-      tiles = pre[b + 1] - pre[b];
-      h = (u - kv * pre[b]) / tiles;
-      first = kv * pre[b] + h * tiles;
-      row = b * kv + h;
-      pages = pages_of(s.a, b) - 1;
-      const Q* src = static_cast<const Q*>(s.q) + b * s.q_stride + static_cast<long long>(h) * s.G * kHeadDim + 4 * lane;
-      typename Four<Q>::Raw raw[NH];
+    const bool more = u + 1 < u1;
+    if (more) {
+      next = locate(u + 1);
+      next_id = look_up(next);
+    }
+    if (at.b * kv + at.h != row) {
+      row = at.b * kv + at.h;
 #pragma unroll
-      for (int n = 0; n < NH; ++n)
-        raw[n] = *reinterpret_cast<const typename Four<Q>::Raw*>(src + (n < s.G ? n : 0) * kHeadDim);
+      for (int n = 0; n < NT; ++n) {
+        const int head = min(n * 8 + g, G - 1);  // rows past the last head repeat it and are dropped
+        const Q* src = static_cast<const Q*>(s.q) + at.b * s.q_stride +
+                       (static_cast<long long>(at.h) * G + head) * kHeadDim + t * C::kPer;
 #pragma unroll
-      for (int n = 0; n < NH; ++n) {
-        Four<Q>::get(raw[n], q[n]);
+        for (int i = 0; i < C::kCount; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q[n][i] = q[n][i] + 0.0;  // -0 counts as 0: its sign bit picks no bound
+          for (int v = 0; v < kQVec; ++v) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + i * 4 * C::kPer + v * (16 / sizeof(Q)));
+            uint32_t* to = &q_raw[n][(i * kQVec + v) * 4];
+            to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
+          }
+      }
+      if constexpr (NT == 1) {
+#pragma unroll
+        for (int x = 0; x < kQWords; ++x) {
+          double d[Word<Q>::kPer];
+          Word<Q>::get(q_raw[0][x], d);
+#pragma unroll
+          for (int y = 0; y < Word<Q>::kPer; ++y) {
+            const bool neg = d[y] < 0.0;
+            q_pos[x * Word<Q>::kPer + y] = neg ? 0.0 : d[y];
+            q_neg[x * Word<Q>::kPer + y] = neg ? d[y] : 0.0;
+          }
+        }
       }
     }
-    const int page0 = (u - first) * kPages;
-    int id = -1;
-    if (lane < kPages && page0 + lane < pages) {
-      id = s.a.table[b * s.a.table_stride + page0 + lane];
-      if (id < 0 || id >= s.a.num_pages) {
-        id = -1;
-        atomicMin(&sm_bad, b);
+    // Four sums of 16 products of 4 dimensions each, so that products need not
+    // wait for one another.
+    double c[NT][4][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) c[n][x][0] = c[n][x][1] = 0.0;
+#pragma unroll
+    for (int x = 0; x < kWords; ++x) {
+      double dl[Word<E>::kPer], dh[Word<E>::kPer];
+      Word<E>::get(lo[x], dl);
+      Word<E>::get(hi[x], dh);
+#pragma unroll
+      for (int y = 0; y < Word<E>::kPer; ++y) {
+        const int k = x * Word<E>::kPer + y;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          double pos, neg;
+          if constexpr (NT == 1) {
+            pos = q_pos[k], neg = q_neg[k];
+          } else {
+            double d[Word<Q>::kPer];
+            Word<Q>::get(q_raw[n][k / Word<Q>::kPer], d);
+            const double v = d[k % Word<Q>::kPer];
+            pos = v < 0.0 ? 0.0 : v, neg = v < 0.0 ? v : 0.0;
+          }
+          mma884(c[n][2 * (k & 1)], pos, dh[y]);
+          mma884(c[n][2 * (k & 1) + 1], neg, dl[y]);
+        }
       }
     }
-    // All pages' bounds are on their way before the first is used; a page that
-    // is none reads page 0 and is dropped below.
-    typename Four<E>::Raw raw_lo[kPages], raw_hi[kPages];
+    if (more) load(next, next_id, lo, hi);
+    // This lane: heads g (+ 8), pages 2 t and 2 t + 1.
+    u64 key[2] = {0ULL, 0ULL};
 #pragma unroll
-    for (int p = 0; p < kPages; ++p) {
-      const int at = max(0, __shfl_sync(0xffffffffu, id, p));
-      const long long off = (static_cast<long long>(at) * kv + h) * kHeadDim + 4 * lane;
-      raw_lo[p] = *reinterpret_cast<const typename Four<E>::Raw*>(static_cast<const E*>(s.lo) + off);
-      raw_hi[p] = *reinterpret_cast<const typename Four<E>::Raw*>(static_cast<const E*>(s.hi) + off);
-    }
-    double sum[32];
+    for (int n = 0; n < NT; ++n) {
+      double sum[2];
 #pragma unroll
-    for (int p = 0; p < kPages; ++p) {
-      double lo[4], hi[4];
-      Four<E>::get(raw_lo[p], lo);
-      Four<E>::get(raw_hi[p], hi);
+      for (int x = 0; x < 2; ++x) sum[x] = (c[n][0][x] + c[n][1][x]) + (c[n][2][x] + c[n][3][x]);
+      const bool here = n * 8 + g < G;
+      // NaN may come of an infinite bound that the query's sign does not use
+      // (0 * inf): those scores are formed again without it.
+      unsigned odd = __ballot_sync(0xffffffffu, here && (sum[0] != sum[0] || sum[1] != sum[1]));
+      while (odd != 0u) {
+        const int from = __ffs(odd) - 1, head = n * 8 + (from >> 2);
+        odd &= odd - 1;
 #pragma unroll
-      for (int n = 0; n < NH; ++n) {
-        double x = 0.0;
+        for (int x = 0; x < 2; ++x) {
+          const int p = max(0, __shfl_sync(0xffffffffu, id, (2 * (from & 3) + x) * 4));
+          const long long off = (static_cast<long long>(p) * kv + at.h) * kHeadDim + 4 * lane;
+          const Q* src = static_cast<const Q*>(s.q) + at.b * s.q_stride +
+                         (static_cast<long long>(at.h) * G + head) * kHeadDim + 4 * lane;
+          double v = 0.0;
+          for (int i = 0; i < 4; ++i) {
+            const double d = value(src[i]);
+            v = fma(d, d < 0.0 ? value(static_cast<const E*>(s.lo)[off + i]) : value(static_cast<const E*>(s.hi)[off + i]), v);
+          }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x = fma(q[n][i], __double2hiint(q[n][i]) < 0 ? lo[i] : hi[i], x);
-        sum[p * NH + n] = x;
+          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == from && sum[x] != sum[x]) sum[x] = v;
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const u64 mine = here ? sortable(sum[x]) : 0ULL;
+        key[x] = mine > key[x] ? mine : key[x];
       }
     }
-    // Lane i ends with the whole warp's sum of value i.
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const bool upper = lane & o;
+    for (int x = 0; x < 2; ++x) {
 #pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const double give = upper ? sum[i] : sum[i + o], keep = upper ? sum[i + o] : sum[i];
-        sum[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      for (int o = 4; o < 32; o <<= 1) {
+        const u64 other = __shfl_xor_sync(0xffffffffu, key[x], o);
+        key[x] = other > key[x] ? other : key[x];
       }
+      const int p = 2 * t + x;
+      const bool there = __shfl_sync(0xffffffffu, id, p * 4) >= 0;
+      if (g == 0 && at.page0 + p < at.pages)
+        s.keys[static_cast<long long>(row) * s.a.max_pages + at.page0 + p] = there ? key[x] : 0ULL;
     }
-    const int p = lane / NH, n = lane % NH;
-    const bool there = __shfl_sync(0xffffffffu, id, p) >= 0;
-    u64 key = there && n < s.G ? sortable(sum[0]) : 0ULL;
-#pragma unroll
-    for (int o = 1; o < NH; o <<= 1) {
-      const u64 other = __shfl_xor_sync(0xffffffffu, key, o);
-      key = other > key ? other : key;
-    }
-    if (n == 0 && page0 + p < pages) s.keys[static_cast<long long>(row) * s.a.max_pages + page0 + p] = key;
+    at = next;
+    id = next_id;
   }
   __syncthreads();
   if (tid == 0) s.bad[blockIdx.x] = sm_bad;
@@ -235,7 +343,7 @@ struct Keys {
 __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs s, int score_ctas, StatusBlock* sb) {
   __shared__ int hist[kBins];
   __shared__ u64 sm_min[kTopThreads / 32], sm_max[kTopThreads / 32];
-  __shared__ int sums[kTopThreads / 32], sums2[kTopThreads / 32];
+  __shared__ int sums[kTopThreads / 32];
   __shared__ int sm_bin, sm_above, sm_in;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
@@ -309,46 +417,55 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     bits = sh;
     __syncthreads();
   }
-  // Places, in page order: kTopThreads pages at a time.
+  // Places, in page order, kHeld stripes of kTopThreads pages at a time: the
+  // counts of every (stripe, warp), one scan of them, and out.  A count holds
+  // the greater ones in its low half, the equal ones in its high half.
+  constexpr int kWarps = kTopThreads / 32;
+  __shared__ unsigned counts[kHeld * kWarps];
+  const unsigned below = (1u << lane) - 1;
   int base_more = 0, base_same = 0;
-  for (int at0 = 0, i = 0; at0 < N; at0 += kTopThreads, ++i) {
-    const int at = at0 + tid;
-    u64 k = 0ULL;
-    if (i < kHeld) {
+  for (int at0 = 0; at0 < N; at0 += kHeld * kTopThreads) {
+    unsigned ranks[kHeld];  // of this thread within (stripe, warp), and its two flags
 #pragma unroll
-      for (int j = 0; j < kHeld; ++j)
-        if (j == i) k = keys.held[j];
-    } else if (at < N) {
-      k = keys.from[at];
+    for (int i = 0; i < kHeld; ++i) {
+      ranks[i] = 0;
+      if (at0 + i * kTopThreads < N) {
+        const int at = at0 + i * kTopThreads + tid;
+        const u64 k = (at0 == 0 ? keys.held[i] : at < N ? keys.from[at] : 0ULL) >> bits;
+        const bool more = at < N && k > prefix, same = at < N && k == prefix;
+        const unsigned m = __ballot_sync(0xffffffffu, more), e = __ballot_sync(0xffffffffu, same);
+        if (lane == 0) counts[i * kWarps + warp] = __popc(m) | (__popc(e) << 16);
+        ranks[i] = __popc(m & below) | (__popc(e & below) << 8) | (more ? 1u << 16 : 0u) | (same ? 1u << 17 : 0u);
+      } else if (lane == 0) {
+        counts[i * kWarps + warp] = 0;
+      }
     }
-    k >>= bits;
-    const bool more = at < N && k > prefix, same = at < N && k == prefix;
-    const unsigned m = __ballot_sync(0xffffffffu, more), e = __ballot_sync(0xffffffffu, same);
-    const unsigned below = (1u << lane) - 1;
-    if (lane == 0) sums[warp] = __popc(m), sums2[warp] = __popc(e);
     __syncthreads();
-    int more_at = base_more + __popc(m & below), same_at = base_same + __popc(e & below);
+    static_assert(kHeld * kWarps <= kTopThreads, "one count per thread");
+    const unsigned mine = tid < kHeld * kWarps ? counts[tid] : 0u;
+    const unsigned before = static_cast<unsigned>(cta_scan(static_cast<int>(mine), sums));
+    if (tid < kHeld * kWarps) counts[tid] = before;
+    if (tid == kHeld * kWarps - 1) sm_above = static_cast<int>(before + mine);
+    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kTopThreads / 32; ++w) {
-      const int x = sums[w], y = sums2[w];
-      if (w < warp) more_at += x, same_at += y;
-      base_more += x, base_same += y;
+    for (int i = 0; i < kHeld; ++i) {
+      const unsigned c = counts[i * kWarps + warp];
+      const int more_at = base_more + static_cast<int>((c & 0xffffu) + (ranks[i] & 0xffu));
+      const int same_at = base_same + static_cast<int>((c >> 16) + ((ranks[i] >> 8) & 0xffu));
+      if ((ranks[i] >> 16 & 1u) || ((ranks[i] >> 17 & 1u) && (all || same_at < need)))
+        out[more_at + min(same_at, need)] = at0 + i * kTopThreads + tid;
     }
-    if (more || (same && (all || same_at < need))) out[more_at + min(same_at, need)] = at;
+    base_more += sm_above & 0xffff;
+    base_same += static_cast<int>(static_cast<unsigned>(sm_above) >> 16);
     __syncthreads();
   }
 }
 
-template <typename Q, typename E, int NH>
-cudaError_t launch_score(const SelectArgs& s, int ctas, cudaStream_t stream) {
-  return launch_pdl(page_score_kernel<Q, E, NH>, dim3(ctas), dim3(kScoreThreads),
-                    static_cast<size_t>(s.a.B + 1) * 4, stream, s);
-}
 template <typename Q, typename E>
 cudaError_t launch_score(const SelectArgs& s, int ctas, cudaStream_t stream) {
-  if (s.G <= 4) return launch_score<Q, E, 4>(s, ctas, stream);
-  if (s.G <= 8) return launch_score<Q, E, 8>(s, ctas, stream);
-  return launch_score<Q, E, 16>(s, ctas, stream);
+  const size_t smem = static_cast<size_t>(s.a.B + 1) * 4;
+  if (s.G <= 8) return launch_pdl(page_score_kernel<Q, E, 1>, dim3(ctas), dim3(kScoreThreads), smem, stream, s);
+  return launch_pdl(page_score_kernel<Q, E, 2>, dim3(ctas), dim3(kScoreThreads), smem, stream, s);
 }
 
 }  // namespace
