@@ -105,7 +105,7 @@ PageWs layout(void* base, int B, int max_pages, int kv, int H) {
   // The scores are gone before the attention that follows writes partial results.
   w.part = reinterpret_cast<float*>(b + o);
   w.keys = reinterpret_cast<unsigned long long*>(b + o);
-  const size_t part = static_cast<size_t>(kMaxWorkers) * 2 * (H / kv) * (kHeadDim + 2) * sizeof(float);
+  const size_t part = static_cast<size_t>(kMaxWorkers) * 2 * (H / kv) * kPartRow * sizeof(float);
   const size_t keys = static_cast<size_t>(B) * kv * max_pages * sizeof(unsigned long long);
   o += align256(part > keys ? part : keys);
   w.bytes = o;

@@ -465,7 +465,6 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
 
   if (tid == 0) sm_bad = kNoBad;
   pdl_wait();
-  pdl_trigger();
   __syncthreads();
   request_scan<kThreads>(B, pre, [&](int b) {
     const int len = s.a.lens[b], use = clamp_len(len, s.a.max_pages, shift);
@@ -653,7 +652,7 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
         __syncthreads();
         const float v_scale = M == kE8 && s.a.v_scale != nullptr ? s.a.v_scale[h] : 1.0f;
         const bool done = whole && row_end;
-        float* part = s.part + static_cast<size_t>(w * 2 + (whole ? 1 : 0)) * (G * (kHeadDim + 2));
+        float* part = s.part + static_cast<size_t>(w * 2 + (whole ? 1 : 0)) * (G * kPartRow);
         for (int head = 0; head < G; ++head) {
           float m = -INFINITY;
 #pragma unroll
@@ -690,113 +689,115 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
     }
     cp_wait<0>();
   }
+  // Only now: CTAs of the join that wait on an SM from the start cost this
+  // kernel a third of its rate (118 us against 83 for 463 MB of E4M3 pages).
+  pdl_trigger();
   __syncthreads();
   if (tid == 0) s.bad[w] = sm_bad;
 }
 
 // Joins the partial results of each (request, KV head) that several workers
 // share, in the order of its keys; writes zeros where there is no token; and
-// the status.  kSplit groups of 128 threads (a dimension each) take every
-// kSplit-th eight parts, whose maxima, sums and outputs are loaded at once.
+// the status.  A warp takes one query head, four dimensions a lane, four parts'
+// maxima, sums and outputs at once.  kSplit = 1: a CTA holds a warp for each
+// head; otherwise kSplit warps share the one head of a CTA, warp g taking
+// every kSplit-th four parts from the g-th, and are joined at the end.
 template <int M, int kSplit>
-__global__ void __launch_bounds__(kHeadDim * kSplit)
+__global__ void __launch_bounds__(kSplit > 1 ? 32 * kSplit : 32 * kMaxGroup)
 page_join_kernel(const AttendArgs s, int workers, StatusBlock* sb) {
-  using Out = typename std::conditional<M == kF32, float, __nv_bfloat16>::type;
-  constexpr int kAhead = 8;
-  __shared__ float sm_m[kSplit], sm_l[kSplit], sm_o[kSplit][kHeadDim];
-  const int tid = threadIdx.x & (kHeadDim - 1), group = threadIdx.x / kHeadDim;
+  constexpr int kAhead = 4;
+  __shared__ float4 sm_o[kSplit][kSplit > 1 ? 32 : 1];
+  __shared__ float sm_m[kSplit], sm_l[kSplit];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = s.G, kv = s.a.kv, B = s.a.B;
+  const int head = kSplit > 1 ? blockIdx.y : warp, group = kSplit > 1 ? warp : 0;
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / kv, h = blockIdx.x - b * kv;
   const int p0 = s.prefix[b], tiles = s.prefix[b + 1] - p0, U = kv * s.prefix[B];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
     int bad = kNoBad;
-    for (int i = threadIdx.x; i < workers; i += 32) bad = min(bad, s.bad[i]);
+    for (int i = lane; i < workers; i += 32) bad = min(bad, s.bad[i]);
     bad = __reduce_min_sync(0xffffffffu, bad);
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       sb->code = bad == kNoBad ? MOVA_OK : MOVA_ERR_DEVICE_CHECK;
       sb->detail = bad == kNoBad ? 0 : bad;
     }
   }
-  const int W = min(workers, U);
-  const int first = blockIdx.y, step = gridDim.y;
-  const long long at0 = static_cast<long long>(blockIdx.x) * G;
-  Out* o = static_cast<Out*>(s.o);
-  if (tiles == 0) {
-    for (int head = first; head < G; head += step) {
-      if (group == 0) o[(at0 + head) * kHeadDim + tid] = from_f32<Out>(0.0f);
-      if (s.lse != nullptr && threadIdx.x == 0) s.lse[at0 + head] = -INFINITY;
+  const long long at = static_cast<long long>(blockIdx.x) * G + head;
+  auto write = [&](float4 v, float lse) {
+    if constexpr (M == kF32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(s.o) + at * kHeadDim + 4 * lane) = v;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(s.o) + at * kHeadDim + 4 * lane) =
+          make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     }
+    if (s.lse != nullptr && lane == 0) s.lse[at] = lse;
+  };
+  if (tiles == 0) {
+    if (group == 0) write(make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY);
     return;
   }
+  const int W = min(workers, U);
   const int u0 = kv * p0 + h * tiles;
   const int w0 = worker_of(u0, W, U), parts = worker_of(u0 + tiles - 1, W, U) - w0 + 1;
   if (parts == 1) return;
-  const int size = G * (kHeadDim + 2);
+  const int size = G * kPartRow;
   // Worker w0 begins this row (its second place), the others continue it.
   const float* part0 = s.part + static_cast<size_t>(w0) * 2 * size;
-  for (int head = first; head < G; head += step) {
-    float m = -INFINITY, l = 0.0f, acc = 0.0f;
-    for (int i0 = group * kAhead; i0 < parts; i0 += kSplit * kAhead) {
-      float pm[kAhead], pl[kAhead], po[kAhead];
+  float m = -INFINITY, l = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  auto scale = [&](float a) { l *= a, acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a; };
+  auto add = [&](float pl, const float4& po, float f) {
+    l = fmaf(pl, f, l);
+    acc.x = fmaf(po.x, f, acc.x), acc.y = fmaf(po.y, f, acc.y);
+    acc.z = fmaf(po.z, f, acc.z), acc.w = fmaf(po.w, f, acc.w);
+  };
+  for (int i0 = group * kAhead; i0 < parts; i0 += kSplit * kAhead) {
+    float pm[kAhead], pl[kAhead];
+    float4 po[kAhead];
 #pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        const int i = min(i0 + x, parts - 1);
-        const float* part = part0 + (2 * i + (i == 0 ? 1 : 0)) * size;
+    for (int x = 0; x < kAhead; ++x) {
+      if (i0 + x < parts) {
+        const float* part = part0 + (2 * (i0 + x) + (i0 + x == 0 ? 1 : 0)) * size;
         pm[x] = part[G * kHeadDim + head];
         pl[x] = part[G * (kHeadDim + 1) + head];
-        po[x] = part[head * kHeadDim + tid];
-      }
-      float top = m;
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x) top = fmaxf(top, pm[x]);
-      const float a = ex2(m - ref_of(top));
-      m = top;
-      l *= a;
-      acc *= a;
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x) {
-        if (i0 + x < parts) {
-          const float f = ex2(pm[x] - ref_of(m));
-          l = fmaf(pl[x], f, l);
-          acc = fmaf(po[x], f, acc);
-        }
+        po[x] = *reinterpret_cast<const float4*>(part + head * kHeadDim + 4 * lane);
+      } else {
+        pm[x] = -INFINITY, pl[x] = 0.0f, po[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
     }
-    if constexpr (kSplit > 1) {
-      if (tid == 0) sm_m[group] = m, sm_l[group] = l;
-      sm_o[group][tid] = acc;
-      __syncthreads();
-      if (group == 0) {
-        float top = m;
+    float top = m;
 #pragma unroll
-        for (int x = 1; x < kSplit; ++x) top = fmaxf(top, sm_m[x]);
-        const float a = ex2(m - ref_of(top));
-        l *= a;
-        acc *= a;
+    for (int x = 0; x < kAhead; ++x) top = fmaxf(top, pm[x]);
+    scale(ex2(m - ref_of(top)));
+    m = top;
 #pragma unroll
-        for (int x = 1; x < kSplit; ++x) {
-          const float f = ex2(sm_m[x] - ref_of(top));
-          l = fmaf(sm_l[x], f, l);
-          acc = fmaf(sm_o[x][tid], f, acc);
-        }
-        m = top;
-      }
-    }
-    if (group == 0) {
-      o[(at0 + head) * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : acc / l);
-      if (s.lse != nullptr && tid == 0) s.lse[at0 + head] = (m + log2f(l)) * kLn2;
-    }
-    if constexpr (kSplit > 1) __syncthreads();
+    for (int x = 0; x < kAhead; ++x) add(pl[x], po[x], ex2(pm[x] - ref_of(m)));
   }
+  if constexpr (kSplit > 1) {
+    sm_o[group][lane] = acc;
+    if (lane == 0) sm_m[group] = m, sm_l[group] = l;
+    __syncthreads();
+    if (group != 0) return;
+    float top = m;
+#pragma unroll
+    for (int x = 1; x < kSplit; ++x) top = fmaxf(top, sm_m[x]);
+    scale(ex2(m - ref_of(top)));
+    m = top;
+#pragma unroll
+    for (int x = 1; x < kSplit; ++x) add(sm_l[x], sm_o[x][lane], ex2(sm_m[x] - ref_of(m)));
+  }
+  write(make_float4(l == 0.0f ? 0.0f : acc.x / l, l == 0.0f ? 0.0f : acc.y / l, l == 0.0f ? 0.0f : acc.z / l,
+                    l == 0.0f ? 0.0f : acc.w / l),
+        (m + log2f(l)) * kLn2);
 }
 
 template <int M, int NT>
 cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
   auto kern = page_attend_kernel<M, NT>;
   static bool done[64] = {false};
-  cudaError_t err = allow_smem(kern, attend_smem<M, NT>(kMaxRequests), done);
+  cudaError_t err = prepare_kernel(kern, attend_smem<M, NT>(kMaxRequests), done);
   if (err != cudaSuccess) return err;
   const size_t smem = attend_smem<M, NT>(s.a.B);
   const int per_sm = static_cast<int>(std::min<size_t>(3, (227 * 1024) / (smem + 2048)));
@@ -808,14 +809,18 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   if (W > most) W = most < 1 ? 1 : most;
   err = launch_pdl(kern, dim3(static_cast<unsigned>(W)), dim3(kThreads), smem, stream, s);
   if (err != cudaSuccess) return err;
-  // A CTA per query head while they all fit at once; few rows can have many
-  // parts each, so those get four groups of threads.
+  // Few rows have many parts each, and leave SMs free: a CTA per head.
   const int rows = s.a.B * s.a.kv;
-  const bool few = static_cast<long long>(rows) * s.G <= sm_count();
-  if (few)
-    return launch_pdl(page_join_kernel<M, 4>, dim3(rows, s.G), dim3(4 * kHeadDim), 0, stream, s, static_cast<int>(W), sb);
-  return launch_pdl(page_join_kernel<M, 1>, dim3(rows, static_cast<long long>(rows) * s.G <= 4096 ? s.G : 1),
-                    dim3(kHeadDim), 0, stream, s, static_cast<int>(W), sb);
+  if (static_cast<long long>(rows) * s.G <= 4LL * sm_count()) {
+    static bool split_done[64] = {false};
+    err = prepare_kernel(page_join_kernel<M, 4>, 0, split_done);
+    if (err != cudaSuccess) return err;
+    return launch_pdl(page_join_kernel<M, 4>, dim3(rows, s.G), dim3(32 * 4), 0, stream, s, static_cast<int>(W), sb);
+  }
+  static bool join_done[64] = {false};
+  err = prepare_kernel(page_join_kernel<M, 1>, 0, join_done);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(page_join_kernel<M, 1>, dim3(rows), dim3(32 * s.G), 0, stream, s, static_cast<int>(W), sb);
 }
 
 }  // namespace

@@ -116,7 +116,7 @@ cudaError_t launch_map_t(const MapArgs& a, int ctas, cudaStream_t stream) {
   static bool done[64] = {false};
   auto kern = page_map_kernel<kThreads, kCluster>;
   constexpr size_t kMost = (kMaxRequests + 1) * 16 + kMaxRequests * 8;
-  cudaError_t err = allow_smem(kern, kMost, done);
+  cudaError_t err = prepare_kernel(kern, kMost, done);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);

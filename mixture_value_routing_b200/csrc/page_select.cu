@@ -113,7 +113,6 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const Sele
   const int B = s.a.B, kv = s.a.kv, G = s.G;
   if (tid == 0) sm_bad = kNoBad;
   pdl_wait();
-  pdl_trigger();
   __syncthreads();
   request_scan<kScoreThreads>(B, pre, [&](int b) {
     const int len = s.a.lens[b];
@@ -287,6 +286,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const Sele
     at = next;
     id = next_id;
   }
+  pdl_trigger();
   __syncthreads();
   if (tid == 0) s.bad[blockIdx.x] = sm_bad;
 }
@@ -318,34 +318,63 @@ __device__ __forceinline__ int cta_scan(int x, int (&sums)[kTopThreads / 32]) {
   return before + incl - x;
 }
 
-// The keys of one (request, KV head): thread t holds keys t + i * kTopThreads,
-// the first kHeld of them in registers, the rest (long requests) in memory.
-constexpr int kHeld = 16;
-struct Keys {
-  const u64* from;
-  int N;
-  u64 held[kHeld];
-  __device__ __forceinline__ Keys(const u64* p, int n) : from(p), N(n) {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int at = threadIdx.x + i * kTopThreads;
-      held[i] = at < N ? from[at] : 0ULL;
-    }
-  }
-  template <typename F> __device__ __forceinline__ void each(F f) const {
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-      if (static_cast<int>(threadIdx.x) + i * kTopThreads < N) f(held[i]);
-    for (int at = threadIdx.x + kHeld * kTopThreads; at < N; at += kTopThreads) f(from[at]);
-  }
+constexpr int kHeld = 16;  // keys of a thread in registers; a long request's others are read again
+constexpr int kTopWarps = kTopThreads / 32;
+
+struct TopShared {
+  int hist[kBins];
+  int sums[kTopWarps];
+  int bin, above, in;
 };
 
+// Radix search among 32-bit values, `bits` of them open, for the `need`
+// greatest: each(f) calls f for every value of this thread.  Returns how many
+// low bits are left open; *prefix the bits above them that the least of the
+// greatest has, *need how many to take of the values with that prefix, *all
+// whether those are all there are.  hist is zero before and after.
+template <typename Each>
+__device__ __forceinline__ int radix_search(Each each, int bits, TopShared& sh, uint32_t* prefix, int* need, bool* all) {
+  *prefix = 0;
+  *all = false;
+  while (bits > 0 && !*all) {
+    const int width = bits < kDigit ? bits : kDigit, low = bits - width;
+    const uint32_t mask = (1u << width) - 1, above_mask = bits == 32 ? 0u : ~0u << bits, want = bits == 32 ? 0u : *prefix << bits;
+    each([&](uint32_t v) {
+      if ((v & above_mask) == want) atomicAdd(&sh.hist[(v >> low) & mask], 1);
+    });
+    __syncthreads();
+    // Thread i holds the bins below kBins - 4 i, from the top.
+    constexpr int kPer = kBins / kTopThreads;
+    const int top_bin = kBins - 1 - static_cast<int>(threadIdx.x) * kPer;
+    int c[kPer], mine = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      c[j] = sh.hist[top_bin - j];
+      mine += c[j];
+    }
+    int above = cta_scan(mine, sh.sums);  // its barrier: every bin has been read
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (above < *need && *need <= above + c[j]) sh.bin = top_bin - j, sh.above = above, sh.in = c[j];
+      above += c[j];
+      sh.hist[top_bin - j] = 0;
+    }
+    __syncthreads();
+    *prefix = (*prefix << width) | static_cast<uint32_t>(sh.bin);
+    *need -= sh.above;
+    *all = *need == sh.in;
+    bits = low;
+    __syncthreads();
+  }
+  return bits;
+}
+
 __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs s, int score_ctas, StatusBlock* sb) {
-  __shared__ int hist[kBins];
-  __shared__ u64 sm_min[kTopThreads / 32], sm_max[kTopThreads / 32];
-  __shared__ int sums[kTopThreads / 32];
-  __shared__ int sm_bin, sm_above, sm_in;
+  __shared__ TopShared sh;
+  __shared__ u64 sm_min[kTopWarps], sm_max[kTopWarps];
+  __shared__ unsigned counts[kHeld * kTopWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kBins; i += kTopThreads) sh.hist[i] = 0;
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && warp == 0) {
@@ -367,61 +396,66 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   if (tid == 0) out[top - 1] = n - 1;
   if (top == 1) return;
   const int N = n - 1;
-  const Keys keys(s.keys + static_cast<long long>(blockIdx.x) * s.a.max_pages, N);
+  const u64* keys = s.keys + static_cast<long long>(blockIdx.x) * s.a.max_pages;
 
-  u64 least = ~0ULL, most_inv = ~0ULL;  // the greatest, as the least complement
-  keys.each([&](u64 k) {
+  // The least and the greatest score: above the bits in which they differ, all agree.
+  u64 held[kHeld], least = ~0ULL, most_inv = ~0ULL;  // the greatest, as the least complement
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int at = tid + i * kTopThreads;
+    held[i] = at < N ? keys[at] : 0ULL;
+  }
+  auto see = [&](u64 k) {
     least = k < least ? k : least;
     most_inv = ~k < most_inv ? ~k : most_inv;
-  });
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (tid + i * kTopThreads < N) see(held[i]);
+  for (int at = tid + kHeld * kTopThreads; at < N; at += kTopThreads) see(keys[at]);
   least = warp_min(least);
   most_inv = warp_min(most_inv);
   if (lane == 0) sm_min[warp] = least, sm_max[warp] = most_inv;
-  for (int i = tid; i < kBins; i += kTopThreads) hist[i] = 0;
   __syncthreads();
+  least = warp_min(sm_min[lane % kTopWarps]);
+  most_inv = warp_min(sm_max[lane % kTopWarps]);
+  const u64 differ = least ^ ~most_inv;
+  const int open = differ == 0 ? 0 : 64 - __clzll(static_cast<long long>(differ));
+
+  // The upper 32 of the open bits settle it, unless scores agree in all of
+  // them; then the rest does, and equal scores go by page number.
+  const int up = max(1, open);
+  auto upper = [&](u64 k) { return static_cast<uint32_t>((k << (64 - up)) >> 32); };
+  const uint32_t rest = open > 32 ? (open == 64 ? ~0u : (1u << (open - 32)) - 1) : 0u;
+  uint32_t v[kHeld];
 #pragma unroll
-  for (int w = 0; w < kTopThreads / 32; ++w) {
-    least = sm_min[w] < least ? sm_min[w] : least;
-    most_inv = sm_max[w] < most_inv ? sm_max[w] : most_inv;
-  }
-  const u64 most = ~most_inv;
-  int bits = least == most ? 0 : 64 - __clzll(static_cast<long long>(least ^ most));  // still open below
-  u64 prefix = bits == 64 ? 0ULL : most >> bits;
-  int need = top - 1;  // to take from the keys that share the prefix
-  bool all = false;    // every one of them
-  while (bits > 0 && !all) {
-    const int width = bits < kDigit ? bits : kDigit, sh = bits - width;
-    keys.each([&](u64 k) {
-      if (bits == 64 || (k >> bits) == prefix) atomicAdd(&hist[static_cast<int>(k >> sh) & ((1 << width) - 1)], 1);
-    });
-    __syncthreads();
-    // Thread i holds the bins below kBins - 4 i, from the top.
-    constexpr int kPer = kBins / kTopThreads;
-    int c[kPer], mine = 0;
+  for (int i = 0; i < kHeld; ++i) v[i] = upper(held[i]);
+  int need = top - 1;
+  bool all;
+  uint32_t p1, p2 = 0;
+  const int r1 = radix_search(
+      [&](auto f) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      c[j] = hist[kBins - 1 - (tid * kPer + j)];
-      mine += c[j];
-    }
-    int above = cta_scan(mine, sums);  // its barrier: every bin has been read
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (above < need && need <= above + c[j]) sm_bin = kBins - 1 - (tid * kPer + j), sm_above = above, sm_in = c[j];
-      above += c[j];
-      hist[kBins - 1 - (tid * kPer + j)] = 0;  // for the next digit
-    }
-    __syncthreads();
-    prefix = (prefix << width) | static_cast<u64>(sm_bin);
-    need -= sm_above;
-    all = need == sm_in;
-    bits = sh;
-    __syncthreads();
-  }
+        for (int i = 0; i < kHeld; ++i)
+          if (tid + i * kTopThreads < N) f(v[i]);
+        for (int at = tid + kHeld * kTopThreads; at < N; at += kTopThreads) f(upper(keys[at]));
+      },
+      open == 0 ? 0 : 32, sh, &p1, &need, &all);
+  const bool second = open > 32 && !all;
+  int r2 = 0;
+  if (second)
+    r2 = radix_search(
+        [&](auto f) {
+          for (int at = tid; at < N; at += kTopThreads) {
+            const u64 k = keys[at];
+            if (upper(k) == p1) f(static_cast<uint32_t>(k) & rest);
+          }
+        },
+        open - 32, sh, &p2, &need, &all);
+
   // Places, in page order, kHeld stripes of kTopThreads pages at a time: the
   // counts of every (stripe, warp), one scan of them, and out.  A count holds
   // the greater ones in its low half, the equal ones in its high half.
-  constexpr int kWarps = kTopThreads / 32;
-  __shared__ unsigned counts[kHeld * kWarps];
   const unsigned below = (1u << lane) - 1;
   int base_more = 0, base_same = 0;
   for (int at0 = 0; at0 < N; at0 += kHeld * kTopThreads) {
@@ -431,41 +465,57 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
       ranks[i] = 0;
       if (at0 + i * kTopThreads < N) {
         const int at = at0 + i * kTopThreads + tid;
-        const u64 k = (at0 == 0 ? keys.held[i] : at < N ? keys.from[at] : 0ULL) >> bits;
-        const bool more = at < N && k > prefix, same = at < N && k == prefix;
+        bool more = false, same = false;
+        if (at < N) {
+          const uint32_t x = open == 0 ? 0u : (at0 == 0 ? v[i] : upper(keys[at])) >> (r1 & 31);
+          more = x > p1;
+          same = x == p1;
+          if (second && same) {
+            const uint32_t y = (static_cast<uint32_t>(keys[at]) & rest) >> r2;
+            more = y > p2;
+            same = y == p2;
+          }
+        }
         const unsigned m = __ballot_sync(0xffffffffu, more), e = __ballot_sync(0xffffffffu, same);
-        if (lane == 0) counts[i * kWarps + warp] = __popc(m) | (__popc(e) << 16);
+        if (lane == 0) counts[i * kTopWarps + warp] = __popc(m) | (__popc(e) << 16);
         ranks[i] = __popc(m & below) | (__popc(e & below) << 8) | (more ? 1u << 16 : 0u) | (same ? 1u << 17 : 0u);
       } else if (lane == 0) {
-        counts[i * kWarps + warp] = 0;
+        counts[i * kTopWarps + warp] = 0;
       }
     }
     __syncthreads();
-    static_assert(kHeld * kWarps <= kTopThreads, "one count per thread");
-    const unsigned mine = tid < kHeld * kWarps ? counts[tid] : 0u;
-    const unsigned before = static_cast<unsigned>(cta_scan(static_cast<int>(mine), sums));
-    if (tid < kHeld * kWarps) counts[tid] = before;
-    if (tid == kHeld * kWarps - 1) sm_above = static_cast<int>(before + mine);
+    static_assert(kHeld * kTopWarps <= kTopThreads, "one count per thread");
+    const unsigned mine = tid < kHeld * kTopWarps ? counts[tid] : 0u;
+    const unsigned before = static_cast<unsigned>(cta_scan(static_cast<int>(mine), sh.sums));
+    if (tid < kHeld * kTopWarps) counts[tid] = before;
+    if (tid == kHeld * kTopWarps - 1) sh.above = static_cast<int>(before + mine);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
-      const unsigned c = counts[i * kWarps + warp];
-      const int more_at = base_more + static_cast<int>((c & 0xffffu) + (ranks[i] & 0xffu));
-      const int same_at = base_same + static_cast<int>((c >> 16) + ((ranks[i] >> 8) & 0xffu));
-      if ((ranks[i] >> 16 & 1u) || ((ranks[i] >> 17 & 1u) && (all || same_at < need)))
-        out[more_at + min(same_at, need)] = at0 + i * kTopThreads + tid;
+      if (ranks[i] >> 16) {
+        const unsigned c = counts[i * kTopWarps + warp];
+        const int more_at = base_more + static_cast<int>((c & 0xffffu) + (ranks[i] & 0xffu));
+        const int same_at = base_same + static_cast<int>((c >> 16) + ((ranks[i] >> 8) & 0xffu));
+        if ((ranks[i] >> 16 & 1u) || all || same_at < need) out[more_at + min(same_at, need)] = at0 + i * kTopThreads + tid;
+      }
     }
-    base_more += sm_above & 0xffff;
-    base_same += static_cast<int>(static_cast<unsigned>(sm_above) >> 16);
+    base_more += sh.above & 0xffff;
+    base_same += static_cast<int>(static_cast<unsigned>(sh.above) >> 16);
     __syncthreads();
   }
 }
 
+template <typename Q, typename E, int NT>
+cudaError_t launch_score_t(const SelectArgs& s, int ctas, cudaStream_t stream) {
+  static bool done[64] = {false};
+  const cudaError_t err = prepare_kernel(page_score_kernel<Q, E, NT>, (kMaxRequests + 1) * 4, done);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(page_score_kernel<Q, E, NT>, dim3(ctas), dim3(kScoreThreads), static_cast<size_t>(s.a.B + 1) * 4,
+                    stream, s);
+}
 template <typename Q, typename E>
 cudaError_t launch_score(const SelectArgs& s, int ctas, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(s.a.B + 1) * 4;
-  if (s.G <= 8) return launch_pdl(page_score_kernel<Q, E, 1>, dim3(ctas), dim3(kScoreThreads), smem, stream, s);
-  return launch_pdl(page_score_kernel<Q, E, 2>, dim3(ctas), dim3(kScoreThreads), smem, stream, s);
+  return s.G <= 8 ? launch_score_t<Q, E, 1>(s, ctas, stream) : launch_score_t<Q, E, 2>(s, ctas, stream);
 }
 
 }  // namespace
@@ -483,6 +533,8 @@ cudaError_t launch_page_select(const void* q, long long q_stride, int G, const P
   if (dt == MOVA_F32) err = launch_score<float, float>(s, n, stream);
   else if (dt == MOVA_BF16) err = launch_score<__nv_bfloat16, __nv_bfloat16>(s, n, stream);
   else err = launch_score<__nv_bfloat16, uint8_t>(s, n, stream);
+  static bool done[64] = {false};
+  if (err == cudaSuccess) err = prepare_kernel(page_top_kernel, 0, done);
   if (err != cudaSuccess) return err;
   return launch_pdl(page_top_kernel, dim3(a.B * a.kv), dim3(kTopThreads), 0, stream, s, n, ws.sb);
 }

@@ -15,10 +15,12 @@ constexpr int kMaxRequests = 4096;
 constexpr int kMaxGroup = 16;    // query heads per KV head
 constexpr int kMaxWorkers = 640;  // CTAs of one attention call
 constexpr int kNoBad = 0x7fffffff;
+// Floats of a partial result per query head: 128 outputs, a maximum and a sum,
+// and two that keep every partial result 16-byte aligned.  The outputs of the
+// G heads come first, then the maxima, then the sums.
+constexpr int kPartRow = kHeadDim + 4;
 
-// Parts of the workspace that the attention kernels share.  `part` holds two
-// partial results per worker: kMaxGroup-bounded G x 128 outputs, then G
-// maxima and G sums (all fp32).
+// Parts of the workspace.  `part` holds two partial results per worker.
 struct PageWs {
   StatusBlock* sb;
   int32_t* bad;     // (kMaxWorkers + 1) first bad request seen by each worker (kNoBad: none)
@@ -124,14 +126,19 @@ __device__ __forceinline__ int clamp_len(int len, int max_pages, int shift) {
   return len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
 }
 
-// Allows `bytes` of dynamic shared memory for `kern`, once per device.
+// Prepares `kern` for its launches, once per device: `bytes` of dynamic shared
+// memory, and the SM's memory split all to shared memory.  Kernels chained by
+// programmatic dependent launch overlap, and an SM changes its split only when
+// idle: one kernel with another split would keep the next one's CTAs off.
 template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes, bool (&done)[64]) {
+cudaError_t prepare_kernel(K kern, size_t bytes, bool (&done)[64]) {
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  if (err == cudaSuccess)
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   if (err == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return err;
 }
