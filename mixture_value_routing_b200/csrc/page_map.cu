@@ -31,10 +31,13 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const MapArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) char smem[];
   __shared__ int sm_bad, sm_used;
-  long long* starts = reinterpret_cast<long long*>(smem);
-  long long* pre = starts + a.B + 1;
-  int* cached = reinterpret_cast<int*>(pre + a.B + 1);
-  int* added = cached + a.B;
+  // Of each request: {tokens before it in the step, pages of the step before
+  // it} (both clipped to kClip), and {cached tokens, pages it has, first entry
+  // of the free list that is its own (-1: refused)}.
+  int2* before = reinterpret_cast<int2*>(smem);                            // (B + 1)
+  int* cached = reinterpret_cast<int*>(before + a.B + 1);
+  int* have = cached + a.B;
+  int* own = have + a.B;
   const int tid = threadIdx.x;
   const int rank = kCluster ? static_cast<int>(blockIdx.x) : 0, CTAs = kCluster ? static_cast<int>(gridDim.x) : 1;
   const int page_size = 1 << a.shift;
@@ -44,51 +47,55 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const MapArgs a) {
   pdl_wait();
   pdl_trigger();
   const int taken = a.taken[0];
-  const bool taken_ok = taken >= 0 && taken <= a.n_free;
-  const long long avail = taken_ok ? a.n_free - taken : 0;
+  const int avail = taken >= 0 && taken <= a.n_free ? min(a.n_free - taken, kClip - 1) : 0;
   const long long cap = static_cast<long long>(a.max_pages) << a.shift;
-  auto pages = [&](long long tokens) { return (tokens + page_size - 1) >> a.shift; };
-  auto fits = [&](int c, int n) { return c >= 0 && n >= 0 && static_cast<long long>(c) + n <= cap; };
 
-  request_scan2<kThreads>(a.B, starts, pre, [&](int b, long long& tokens, long long& need) {
+  request_scan2<kThreads>(a.B, before, [&](int b, long long& tokens, long long& need) {
     const int c = a.cached[b], n = a.added[b];
+    const bool fits = c >= 0 && n >= 0 && static_cast<long long>(c) + n <= cap;
     cached[b] = c;
-    added[b] = n;
+    have[b] = fits ? (c + page_size - 1) >> a.shift : -1;
     tokens = n < 0 ? 0 : n;
-    need = fits(c, n) ? pages(static_cast<long long>(c) + n) - pages(c) : 0LL;
+    need = fits ? ((c + n + page_size - 1) >> a.shift) - have[b] : 0;
   });
-  // Whether request b gets its pages; its share of the free list is [pre[b], pre[b + 1]).
-  auto granted = [&](int b) {
-    return fits(cached[b], added[b]) && (pre[b + 1] == pre[b] || pre[b + 1] <= avail);
-  };
   for (int b = tid; b < a.B; b += kThreads) {
-    const bool ok = granted(b);
-    if (!ok || starts[b + 1] > a.T) atomicMin(&sm_bad, b);
+    const int end = before[b + 1].y, c = cached[b], n = a.added[b];
+    const bool ok = have[b] >= 0 && (((c + n + page_size - 1) >> a.shift) == have[b] || end <= avail);
+    own[b] = ok ? max(taken, 0) + before[b].y : -1;
+    if (!ok || before[b + 1].x > a.T) atomicMin(&sm_bad, b);
     // The last request within the free pages: what is handed out.
-    if (pre[b + 1] <= avail && (b + 1 == a.B || pre[b + 2] > avail)) sm_used = static_cast<int>(pre[b + 1]);
-    if (rank == 0) a.lens[b] = ok ? cached[b] + added[b] : max(cached[b], 0);
+    if (end <= avail && (b + 1 == a.B || before[b + 2].y > avail)) sm_used = end;
+    if (rank == 0) a.lens[b] = ok ? c + n : max(c, 0);
   }
   if (rank == 0)
-    for (int b = tid; b <= a.B; b += kThreads)
-      a.starts[b] = static_cast<int>(starts[b] > 0x7fffffff ? 0x7fffffff : starts[b]);
+    for (int b = tid; b <= a.B; b += kThreads) a.starts[b] = before[b].x;
   __syncthreads();
   const int used = sm_used;
   const int all = CTAs * kThreads, me = rank * kThreads + tid;
+  // The last request with at most x before it, by the chosen count.
+  auto find = [&](int x, bool by_page) {
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((by_page ? before[mid].y : before[mid].x) <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
   for (int x = me; x < used; x += all) {
-    const int b = request_of(pre, a.B, static_cast<long long>(x));
-    const long long j = pages(cached[b]) + x - pre[b];
-    a.table[b * a.table_stride + j] = a.free_pages[taken + x];
+    const int b = find(x, true);
+    a.table[b * a.table_stride + have[b] + x - before[b].y] = a.free_pages[taken + x];
   }
-  const long long total = starts[a.B];
-  for (long long i = me; i < a.T; i += all) {
+  const int total = before[a.B].x;
+  for (long long i64 = me; i64 < a.T; i64 += all) {
+    const int i = static_cast<int>(i64);
     int slot = -1, pos = -1;
     if (i < total) {
-      const int b = request_of(starts, a.B, i);
-      const int c = cached[b];
-      if (granted(b)) {
-        pos = static_cast<int>(c + i - starts[b]);
-        const int j = pos >> a.shift, have = static_cast<int>(pages(c));
-        const int page = j < have ? a.table[b * a.table_stride + j] : a.free_pages[taken + pre[b] + j - have];
+      const int b = find(i, false);
+      const int first = own[b];
+      if (first >= 0) {
+        pos = cached[b] + i - before[b].x;
+        const int j = pos >> a.shift;
+        const int page = j < have[b] ? a.table[b * a.table_stride + j] : a.free_pages[first + j - have[b]];
         if (page >= 0 && page < a.num_pages)
           slot = (page << a.shift) + (pos & (page_size - 1));
         else
@@ -115,13 +122,13 @@ template <int kThreads, bool kCluster>
 cudaError_t launch_map_t(const MapArgs& a, int ctas, cudaStream_t stream) {
   static bool done[64] = {false};
   auto kern = page_map_kernel<kThreads, kCluster>;
-  constexpr size_t kMost = (kMaxRequests + 1) * 16 + kMaxRequests * 8;
+  constexpr size_t kMost = (kMaxRequests + 1) * 8 + kMaxRequests * 12;
   cudaError_t err = prepare_kernel(kern, kMost, done);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(a.B + 1) * 16 + static_cast<size_t>(a.B) * 8;
+  cfg.dynamicSmemBytes = static_cast<size_t>(a.B + 1) * 8 + static_cast<size_t>(a.B) * 12;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

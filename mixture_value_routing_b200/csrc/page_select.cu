@@ -17,8 +17,10 @@
 //
 // Selection: one CTA per (request, KV head) finds the K-th greatest score by
 // radix search: the digits start below the bits that the least and the
-// greatest score share, so two or three passes of 11 bits settle it; then one
-// scan places the selected pages in order.  No atomics decide an order.
+// greatest score share, so three or four passes of 8 bits settle it.  Latency
+// bounds it (a few thousand scores, in registers): a warp owns a contiguous run
+// of pages, so the passes and the placing in order need one barrier each.  No
+// atomics decide an order.
 #include <math.h>
 
 #include "paged.cuh"
@@ -29,10 +31,11 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kScorePerSm = 2;
+// CTAs of the score kernel an SM: by the registers of its NT tiles of heads.
+constexpr int score_per_sm(int NT) { return NT == 1 ? 3 : 2; }
 constexpr int kPages = 8;  // of one batch
 constexpr int kTopThreads = 512;
-constexpr int kDigit = 11;
+constexpr int kDigit = 8;
 constexpr int kBins = 1 << kDigit;
 
 using u64 = unsigned long long;
@@ -99,14 +102,34 @@ template <typename E> struct Chunk {
   static constexpr int kCount = kHeadDim / kPer / 4;
 };
 
-// NT: tiles of 8 heads.  One tile's q stays in registers in fp64, split by
-// sign; two tiles' q stays as loaded and is converted for each batch of pages.
+// An element of q as it stays in registers, and its positive and negative part
+// in fp64.  bf16: the upper word of the fp64 value, whose lower word is zero;
+// fp32: as it is, converted at each use.
+template <typename Q> struct Part;
+template <> struct Part<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t keep(double d) { return static_cast<uint32_t>(__double2hiint(d)); }
+  static __device__ __forceinline__ void get(uint32_t w, double& pos, double& neg) {
+    const int sign = static_cast<int>(w) >> 31;  // all ones below zero
+    pos = __hiloint2double(static_cast<int>(w) & ~sign, 0);
+    neg = __hiloint2double(static_cast<int>(w) & sign, 0);
+  }
+};
+template <> struct Part<float> {
+  static __device__ __forceinline__ uint32_t keep(double d) { return __float_as_uint(static_cast<float>(d)); }
+  static __device__ __forceinline__ void get(uint32_t w, double& pos, double& neg) {
+    const int sign = static_cast<int>(w) >> 31;
+    const double d = __uint_as_float(w);
+    pos = __hiloint2double(__double2hiint(d) & ~sign, __double2loint(d) & ~sign);
+    neg = __hiloint2double(__double2hiint(d) & sign, __double2loint(d) & sign);
+  }
+};
+
+// NT: tiles of 8 heads.
 template <typename Q, typename E, int NT>
-__global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const SelectArgs s) {
+__global__ void __launch_bounds__(kScoreThreads, score_per_sm(NT)) page_score_kernel(const SelectArgs s) {
   using C = Chunk<E>;
-  constexpr int kWords = C::kCount * 4;                       // 32-bit words of a lane's bounds
-  constexpr int kQWords = 32 / Word<Q>::kPer;                 // and of its 32 elements of q
-  constexpr int kQVec = kQWords / C::kCount / 4;              // 16-byte loads of q per chunk
+  constexpr int kWords = C::kCount * 4;                          // 32-bit words of a lane's bounds
+  constexpr int kQVec = 32 / Word<Q>::kPer / C::kCount / 4;      // 16-byte loads of q per chunk
   extern __shared__ int pre[];
   __shared__ int sm_bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -143,29 +166,28 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const Sele
     atomicMin(&sm_bad, r.b);
     return -1;
   };
-  // A page that is none reads page 0; its score is dropped.
-  auto load = [&](const At& r, int id, uint32_t (&lo)[kWords], uint32_t (&hi)[kWords]) {
-    const long long off = (static_cast<long long>(max(id, 0)) * kv + r.h) * kHeadDim + t * C::kPer;
-    const E* pl = static_cast<const E*>(s.lo) + off;
-    const E* ph = static_cast<const E*>(s.hi) + off;
-#pragma unroll
-    for (int i = 0; i < C::kCount; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(pl + i * 4 * C::kPer);
-      const uint4 y = *reinterpret_cast<const uint4*>(ph + i * 4 * C::kPer);
-      lo[4 * i] = x.x, lo[4 * i + 1] = x.y, lo[4 * i + 2] = x.z, lo[4 * i + 3] = x.w;
-      hi[4 * i] = y.x, hi[4 * i + 1] = y.y, hi[4 * i + 2] = y.z, hi[4 * i + 3] = y.w;
-    }
+  // This lane's first bounds in page `id`; a page that is none reads page 0, and
+  // its score is dropped.
+  auto offset = [&](const At& r, int id) {
+    return (static_cast<long long>(max(id, 0)) * kv + r.h) * kHeadDim + t * C::kPer;
+  };
+  uint32_t lo[kWords], hi[kWords];
+  auto load = [&](long long off, int i) {
+    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const E*>(s.lo) + off + i * 4 * C::kPer);
+    const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const E*>(s.hi) + off + i * 4 * C::kPer);
+    lo[4 * i] = x.x, lo[4 * i + 1] = x.y, lo[4 * i + 2] = x.z, lo[4 * i + 3] = x.w;
+    hi[4 * i] = y.x, hi[4 * i + 1] = y.y, hi[4 * i + 2] = y.z, hi[4 * i + 3] = y.w;
   };
 
-  uint32_t q_raw[NT][kQWords];
-  double q_pos[NT == 1 ? 32 : 1], q_neg[NT == 1 ? 32 : 1];
-  uint32_t lo[kWords], hi[kWords];
+  uint32_t q[NT][32];
   At at{}, next{};
   int id = -1, next_id = -1, row = -1;
   if (u0 < u1) {
     at = locate(u0);
     id = look_up(at);
-    load(at, id, lo, hi);
+    const long long off = offset(at, id);
+#pragma unroll
+    for (int i = 0; i < C::kCount; ++i) load(off, i);
   }
   for (int u = u0; u < u1; ++u) {
     const bool more = u + 1 < u1;
@@ -185,22 +207,16 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const Sele
 #pragma unroll
           for (int v = 0; v < kQVec; ++v) {
             const uint4 x = *reinterpret_cast<const uint4*>(src + i * 4 * C::kPer + v * (16 / sizeof(Q)));
-            uint32_t* to = &q_raw[n][(i * kQVec + v) * 4];
-            to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
-          }
-      }
-      if constexpr (NT == 1) {
+            const uint32_t words[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int x = 0; x < kQWords; ++x) {
-          double d[Word<Q>::kPer];
-          Word<Q>::get(q_raw[0][x], d);
+            for (int y = 0; y < 4; ++y) {
+              double d[Word<Q>::kPer];
+              Word<Q>::get(words[y], d);
 #pragma unroll
-          for (int y = 0; y < Word<Q>::kPer; ++y) {
-            const bool neg = d[y] < 0.0;
-            q_pos[x * Word<Q>::kPer + y] = neg ? 0.0 : d[y];
-            q_neg[x * Word<Q>::kPer + y] = neg ? d[y] : 0.0;
+              for (int z = 0; z < Word<Q>::kPer; ++z)
+                q[n][((i * kQVec + v) * 4 + y) * Word<Q>::kPer + z] = Part<Q>::keep(d[z]);
+            }
           }
-        }
       }
     }
     // Four sums of 16 products of 4 dimensions each, so that products need not
@@ -210,31 +226,31 @@ __global__ void __launch_bounds__(kScoreThreads, 2) page_score_kernel(const Sele
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int x = 0; x < 4; ++x) c[n][x][0] = c[n][x][1] = 0.0;
+    // Conversions run a word ahead of the products, whose latency they have; a
+    // chunk's registers take the next pages' bounds as soon as it is used.
+    const long long next_off = more ? offset(next, next_id) : 0;
+    double dl[2][Word<E>::kPer], dh[2][Word<E>::kPer];
+    Word<E>::get(lo[0], dl[0]);
+    Word<E>::get(hi[0], dh[0]);
 #pragma unroll
     for (int x = 0; x < kWords; ++x) {
-      double dl[Word<E>::kPer], dh[Word<E>::kPer];
-      Word<E>::get(lo[x], dl);
-      Word<E>::get(hi[x], dh);
+      if (x + 1 < kWords) {
+        Word<E>::get(lo[x + 1], dl[(x + 1) & 1]);
+        Word<E>::get(hi[x + 1], dh[(x + 1) & 1]);
+      }
 #pragma unroll
       for (int y = 0; y < Word<E>::kPer; ++y) {
         const int k = x * Word<E>::kPer + y;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           double pos, neg;
-          if constexpr (NT == 1) {
-            pos = q_pos[k], neg = q_neg[k];
-          } else {
-            double d[Word<Q>::kPer];
-            Word<Q>::get(q_raw[n][k / Word<Q>::kPer], d);
-            const double v = d[k % Word<Q>::kPer];
-            pos = v < 0.0 ? 0.0 : v, neg = v < 0.0 ? v : 0.0;
-          }
-          mma884(c[n][2 * (k & 1)], pos, dh[y]);
-          mma884(c[n][2 * (k & 1) + 1], neg, dl[y]);
+          Part<Q>::get(q[n][k], pos, neg);
+          mma884(c[n][2 * (k & 1)], pos, dh[x & 1][y]);
+          mma884(c[n][2 * (k & 1) + 1], neg, dl[x & 1][y]);
         }
       }
+      if (more && (x & 3) == 3) load(next_off, x >> 2);
     }
-    if (more) load(next, next_id, lo, hi);
     // This lane: heads g (+ 8), pages 2 t and 2 t + 1.
     u64 key[2] = {0ULL, 0ULL};
 #pragma unroll
@@ -300,81 +316,70 @@ __device__ __forceinline__ u64 warp_min(u64 x) {
   return x;
 }
 
-// Exclusive prefix sum of x over the CTA.  `sums` is the caller's alone.
-__device__ __forceinline__ int cta_scan(int x, int (&sums)[kTopThreads / 32]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = x;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) sums[warp] = incl;
-  __syncthreads();
-  int before = 0;
-#pragma unroll
-  for (int w = 0; w < kTopThreads / 32; ++w)
-    if (w < warp) before += sums[w];
-  return before + incl - x;
-}
-
 constexpr int kHeld = 16;  // keys of a thread in registers; a long request's others are read again
 constexpr int kTopWarps = kTopThreads / 32;
 
-struct TopShared {
-  int hist[kBins];
-  int sums[kTopWarps];
-  int bin, above, in;
-};
-
-// Radix search among 32-bit values, `bits` of them open, for the `need`
-// greatest: each(f) calls f for every value of this thread.  Returns how many
-// low bits are left open; *prefix the bits above them that the least of the
-// greatest has, *need how many to take of the values with that prefix, *all
-// whether those are all there are.  hist is zero before and after.
+// Radix search among 32-bit values for the `need` greatest: each(f) calls f for
+// every value of this thread, whose upper `bits` are searched.  Returns how
+// many of them are left open; *prefix the bits above those that the least of
+// the greatest has, *need how many to take of the values with that prefix,
+// *all whether those are all there are.  hist: one zeroed row for each digit.
+// Every warp reads the counts and comes to the same answer, so a digit costs
+// one barrier.
 template <typename Each>
-__device__ __forceinline__ int radix_search(Each each, int bits, TopShared& sh, uint32_t* prefix, int* need, bool* all) {
+__device__ __forceinline__ int radix_search(Each each, int bits, int (*hist)[kBins], uint32_t* prefix, int* need,
+                                            bool* all) {
+  const int lane = threadIdx.x & 31;
   *prefix = 0;
   *all = false;
-  while (bits > 0 && !*all) {
-    const int width = bits < kDigit ? bits : kDigit, low = bits - width;
-    const uint32_t mask = (1u << width) - 1, above_mask = bits == 32 ? 0u : ~0u << bits, want = bits == 32 ? 0u : *prefix << bits;
+  for (int digit = 0; bits > 0 && !*all; ++digit) {
+    const int width = min(bits, kDigit), low = bits - width;
+    const uint32_t mask = (1u << width) - 1, above_mask = bits == 32 ? 0u : ~0u << bits;
+    const uint32_t want = bits == 32 ? 0u : *prefix << bits;
     each([&](uint32_t v) {
-      if ((v & above_mask) == want) atomicAdd(&sh.hist[(v >> low) & mask], 1);
+      if ((v & above_mask) == want) atomicAdd(&hist[digit][(v >> low) & mask], 1);
     });
     __syncthreads();
-    // Thread i holds the bins below kBins - 4 i, from the top.
-    constexpr int kPer = kBins / kTopThreads;
-    const int top_bin = kBins - 1 - static_cast<int>(threadIdx.x) * kPer;
+    // Lane i holds the kPer bins below kBins - kPer * i, from the top.
+    constexpr int kPer = kBins / 32;
+    const int top_bin = kBins - 1 - lane * kPer;
     int c[kPer], mine = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      c[j] = sh.hist[top_bin - j];
+      c[j] = hist[digit][top_bin - j];
       mine += c[j];
     }
-    int above = cta_scan(mine, sh.sums);  // its barrier: every bin has been read
+    int above = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, above, o);
+      if (lane >= o) above += up;
+    }
+    above -= mine;
+    int bin = 0, left = 0, in = 0;
+    bool here = false;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      if (above < *need && *need <= above + c[j]) sh.bin = top_bin - j, sh.above = above, sh.in = c[j];
+      if (above < *need && *need <= above + c[j]) here = true, bin = top_bin - j, left = *need - above, in = c[j];
       above += c[j];
-      sh.hist[top_bin - j] = 0;
     }
-    __syncthreads();
-    *prefix = (*prefix << width) | static_cast<uint32_t>(sh.bin);
-    *need -= sh.above;
-    *all = *need == sh.in;
+    const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    bin = __shfl_sync(0xffffffffu, bin, from);
+    *need = __shfl_sync(0xffffffffu, left, from);
+    *all = *need == __shfl_sync(0xffffffffu, in, from);
+    *prefix = (*prefix << width) | static_cast<uint32_t>(bin);
     bits = low;
-    __syncthreads();
   }
   return bits;
 }
 
 __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs s, int score_ctas, StatusBlock* sb) {
-  __shared__ TopShared sh;
+  constexpr int kDigits = 32 / kDigit;
+  __shared__ int hist[2 * kDigits][kBins];
   __shared__ u64 sm_min[kTopWarps], sm_max[kTopWarps];
-  __shared__ unsigned counts[kHeld * kTopWarps];
+  __shared__ int2 sm_count[kTopWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kBins; i += kTopThreads) sh.hist[i] = 0;
+  for (int i = tid; i < 2 * kDigits * kBins; i += kTopThreads) (&hist[0][0])[i] = 0;
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && warp == 0) {
@@ -397,22 +402,24 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   if (top == 1) return;
   const int N = n - 1;
   const u64* keys = s.keys + static_cast<long long>(blockIdx.x) * s.a.max_pages;
+  // Each warp has a contiguous run of `span` stripes of 32 pages.
+  const int span = (N + kTopThreads - 1) / kTopThreads, first = warp * span * 32 + lane;
 
   // The least and the greatest score: above the bits in which they differ, all agree.
   u64 held[kHeld], least = ~0ULL, most_inv = ~0ULL;  // the greatest, as the least complement
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i) {
-    const int at = tid + i * kTopThreads;
-    held[i] = at < N ? keys[at] : 0ULL;
-  }
+  for (int i = 0; i < kHeld; ++i) held[i] = i < span && first + 32 * i < N ? keys[first + 32 * i] : 0ULL;
   auto see = [&](u64 k) {
     least = k < least ? k : least;
     most_inv = ~k < most_inv ? ~k : most_inv;
   };
 #pragma unroll
-  for (int i = 0; i < kHeld; ++i)
-    if (tid + i * kTopThreads < N) see(held[i]);
-  for (int at = tid + kHeld * kTopThreads; at < N; at += kTopThreads) see(keys[at]);
+  for (int i = 0; i < kHeld; ++i) {
+    if (i >= span) break;
+    if (first + 32 * i < N) see(held[i]);
+  }
+  for (int i = kHeld; i < span; ++i)
+    if (first + 32 * i < N) see(keys[first + 32 * i]);
   least = warp_min(least);
   most_inv = warp_min(most_inv);
   if (lane == 0) sm_min[warp] = least, sm_max[warp] = most_inv;
@@ -436,73 +443,65 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   const int r1 = radix_search(
       [&](auto f) {
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-          if (tid + i * kTopThreads < N) f(v[i]);
-        for (int at = tid + kHeld * kTopThreads; at < N; at += kTopThreads) f(upper(keys[at]));
+        for (int i = 0; i < kHeld; ++i) {
+          if (i >= span) break;
+          if (first + 32 * i < N) f(v[i]);
+        }
+        for (int i = kHeld; i < span; ++i)
+          if (first + 32 * i < N) f(upper(keys[first + 32 * i]));
       },
-      open == 0 ? 0 : 32, sh, &p1, &need, &all);
+      open == 0 ? 0 : 32, hist, &p1, &need, &all);
   const bool second = open > 32 && !all;
   int r2 = 0;
   if (second)
     r2 = radix_search(
         [&](auto f) {
-          for (int at = tid; at < N; at += kTopThreads) {
-            const u64 k = keys[at];
+          for (int i = 0; i < span; ++i) {
+            if (first + 32 * i >= N) continue;
+            const u64 k = keys[first + 32 * i];
             if (upper(k) == p1) f(static_cast<uint32_t>(k) & rest);
           }
         },
-        open - 32, sh, &p2, &need, &all);
+        open - 32, hist + kDigits, &p2, &need, &all);
 
-  // Places, in page order, kHeld stripes of kTopThreads pages at a time: the
-  // counts of every (stripe, warp), one scan of them, and out.  A count holds
-  // the greater ones in its low half, the equal ones in its high half.
-  const unsigned below = (1u << lane) - 1;
-  int base_more = 0, base_same = 0;
-  for (int at0 = 0; at0 < N; at0 += kHeld * kTopThreads) {
-    unsigned ranks[kHeld];  // of this thread within (stripe, warp), and its two flags
+  // Whether key i of this thread is above the threshold (1), at it (2), or neither.
+  auto place = [&](int i, uint32_t value) {
+    if (first + 32 * i >= N) return 0;
+    uint32_t x = open == 0 ? 0u : value >> r1, p = p1;
+    if (second && x == p) x = (static_cast<uint32_t>(keys[first + 32 * i]) & rest) >> r2, p = p2;
+    return x > p ? 1 : x == p ? 2 : 0;
+  };
+  auto value_of = [&](int i) { return upper(keys[first + 32 * i]); };
+  // The warps' counts, one barrier, and out, in page order.
+  int2 mine = make_int2(0, 0);
+  auto count = [&](int at) {
+    mine.x += __popc(__ballot_sync(0xffffffffu, at == 1));
+    mine.y += __popc(__ballot_sync(0xffffffffu, at == 2));
+  };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      ranks[i] = 0;
-      if (at0 + i * kTopThreads < N) {
-        const int at = at0 + i * kTopThreads + tid;
-        bool more = false, same = false;
-        if (at < N) {
-          const uint32_t x = open == 0 ? 0u : (at0 == 0 ? v[i] : upper(keys[at])) >> (r1 & 31);
-          more = x > p1;
-          same = x == p1;
-          if (second && same) {
-            const uint32_t y = (static_cast<uint32_t>(keys[at]) & rest) >> r2;
-            more = y > p2;
-            same = y == p2;
-          }
-        }
-        const unsigned m = __ballot_sync(0xffffffffu, more), e = __ballot_sync(0xffffffffu, same);
-        if (lane == 0) counts[i * kTopWarps + warp] = __popc(m) | (__popc(e) << 16);
-        ranks[i] = __popc(m & below) | (__popc(e & below) << 8) | (more ? 1u << 16 : 0u) | (same ? 1u << 17 : 0u);
-      } else if (lane == 0) {
-        counts[i * kTopWarps + warp] = 0;
-      }
-    }
-    __syncthreads();
-    static_assert(kHeld * kTopWarps <= kTopThreads, "one count per thread");
-    const unsigned mine = tid < kHeld * kTopWarps ? counts[tid] : 0u;
-    const unsigned before = static_cast<unsigned>(cta_scan(static_cast<int>(mine), sh.sums));
-    if (tid < kHeld * kTopWarps) counts[tid] = before;
-    if (tid == kHeld * kTopWarps - 1) sh.above = static_cast<int>(before + mine);
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      if (ranks[i] >> 16) {
-        const unsigned c = counts[i * kTopWarps + warp];
-        const int more_at = base_more + static_cast<int>((c & 0xffffu) + (ranks[i] & 0xffu));
-        const int same_at = base_same + static_cast<int>((c >> 16) + ((ranks[i] >> 8) & 0xffu));
-        if ((ranks[i] >> 16 & 1u) || all || same_at < need) out[more_at + min(same_at, need)] = at0 + i * kTopThreads + tid;
-      }
-    }
-    base_more += sh.above & 0xffff;
-    base_same += static_cast<int>(static_cast<unsigned>(sh.above) >> 16);
-    __syncthreads();
+  for (int i = 0; i < kHeld; ++i) {
+    if (i >= span) break;
+    count(place(i, v[i]));
   }
+  for (int i = kHeld; i < span; ++i) count(place(i, first + 32 * i < N ? value_of(i) : 0u));
+  if (lane == 0) sm_count[warp] = mine;
+  __syncthreads();
+  int more = 0, same = 0;
+  for (int w = 0; w < warp; ++w) more += sm_count[w].x, same += sm_count[w].y;
+  const unsigned below = (1u << lane) - 1;
+  auto write = [&](int i, int at) {
+    const unsigned m = __ballot_sync(0xffffffffu, at == 1), e = __ballot_sync(0xffffffffu, at == 2);
+    const int more_at = more + __popc(m & below), same_at = same + __popc(e & below);
+    if (at == 1 || (at == 2 && (all || same_at < need))) out[more_at + min(same_at, need)] = first + 32 * i;
+    more += __popc(m);
+    same += __popc(e);
+  };
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    if (i >= span) break;
+    write(i, place(i, v[i]));
+  }
+  for (int i = kHeld; i < span; ++i) write(i, place(i, first + 32 * i < N ? value_of(i) : 0u));
 }
 
 template <typename Q, typename E, int NT>
@@ -525,7 +524,7 @@ cudaError_t launch_page_select(const void* q, long long q_stride, int G, const P
                                cudaStream_t stream) {
   const SelectArgs s{a, q, q_stride, G, top, lo, hi, ws.keys, ws.bad, picked};
   const long long most = (static_cast<long long>(a.B) * a.kv * a.max_pages + kScoreWarps - 1) / kScoreWarps;
-  long long ctas = sm_count() * static_cast<long long>(kScorePerSm);
+  long long ctas = static_cast<long long>(sm_count()) * score_per_sm(G <= 8 ? 1 : 2);
   if (ctas > kMaxWorkers) ctas = kMaxWorkers;
   if (ctas > most) ctas = most < 1 ? 1 : most;
   const int n = static_cast<int>(ctas);

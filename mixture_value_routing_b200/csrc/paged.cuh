@@ -78,12 +78,15 @@ __device__ __forceinline__ void request_scan(int B, T* pre, F count) {
   __syncthreads();
 }
 
-// As request_scan, of two counts per request at once.
+// As request_scan, of two counts per request at once; sums in 64 bits, stored
+// clipped to kClip (more than any count of pages or tokens that is used).
+constexpr int kClip = 0x7fffffff;
 template <int kThreads, typename F>
-__device__ __forceinline__ void request_scan2(int B, long long* pre1, long long* pre2, F count) {
+__device__ __forceinline__ void request_scan2(int B, int2* pre, F count) {
   __shared__ long long warp_sum[2][kThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long carry1 = 0, carry2 = 0;
+  auto clip = [](long long x) { return static_cast<int>(x > kClip ? kClip : x); };
   for (int base = 0; base < B; base += kThreads) {
     const int b = base + tid;
     long long c1 = 0, c2 = 0;
@@ -103,10 +106,10 @@ __device__ __forceinline__ void request_scan2(int B, long long* pre1, long long*
       if (w < warp) before1 += s1, before2 += s2;
       carry1 += s1, carry2 += s2;
     }
-    if (b < B) pre1[b] = before1 + i1 - c1, pre2[b] = before2 + i2 - c2;
+    if (b < B) pre[b] = make_int2(clip(before1 + i1 - c1), clip(before2 + i2 - c2));
     __syncthreads();
   }
-  if (tid == 0) pre1[B] = carry1, pre2[B] = carry2;
+  if (tid == 0) pre[B] = make_int2(clip(carry1), clip(carry2));
   __syncthreads();
 }
 

@@ -97,6 +97,19 @@ def test_map_refusals(api, what):
     check_map(api, cached, added, table, free, taken, 16, num, T)
 
 
+def test_map_sums_past_32_bits(api):
+    """Forty requests of 2^30 tokens each want 40 * 2^26 pages: none has room, and
+    none is taken for one that needs no page once the sum has passed 32 bits."""
+    B, width = 40, 1 << 26
+    table = torch.empty(B, width, dtype=I32, device="cuda")
+    added = ints([1 << 30] * (B - 1) + [17])
+    lens, starts, slots, positions, taken = api.page_map(ints([0] * B), added, table, ints([3, 4, 5]), ints([1]), 16, 10, 50)
+    assert api.get_status() == ("MOVA_ERR_DEVICE_CHECK", 0)
+    assert lens.tolist() == [0] * B and taken.tolist() == [1]
+    assert starts.tolist() == [0, 1 << 30] + [2 ** 31 - 1] * (B - 1)
+    assert slots.tolist() == positions.tolist() == [-1] * 50
+
+
 def test_map_without_requests_or_tokens(api):
     check_map(api, [], [], [], [1], 0, 16, 10, 5)
     check_map(api, [3], [0], [[1]], [], 0, 16, 10, 0)
