@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import struct
 from typing import Optional
 
 import torch
@@ -479,6 +480,13 @@ _I32 = torch.int32
 _RSQRT_128 = 0.08838834764831845
 
 
+# mova_pages, packed: the fields of _lib.Pages.
+_PAGES = struct.Struct("@QQiiiiqqQQ")
+
+
+# The checks below are written for the common case to cost little: one test of
+# everything, and only if it fails a second look that says what is wrong.
+
 def _on(index: int, **tensors) -> None:
     """Every tensor on CUDA device `index`: the library sees addresses only."""
     for name, t in tensors.items():
@@ -494,9 +502,13 @@ def _elsewhere(t: torch.Tensor) -> bool:
     return index != _current_device()
 
 
-def _vector(t: torch.Tensor, name: str, n: int, dtype=_I32) -> None:
+def _vector(t: torch.Tensor, name: str, n: int, index: int, dtype=_I32) -> int:
+    """The address of a contiguous vector of n elements on device `index`."""
     if t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} vector of {n}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != index:
+        _on(index, **{name: t})
+    return t.data_ptr()
 
 
 def _row_stride(t: torch.Tensor, name: str, width: int) -> int:
@@ -530,7 +542,7 @@ def _heads(t: torch.Tensor, name: str, dtype):
 
 
 def _pages(index: int, k_cache, v_cache=None, k_scale=None, v_scale=None):
-    """The mova_pages of a cache, and its (num_pages, KV heads)."""
+    """The packed mova_pages of a cache, and its (num_pages, KV heads)."""
     dtype, shape = k_cache.dtype, k_cache.shape
     if dtype not in _CACHE_IO:
         raise ValueError(f"k_cache: dtype {dtype} not in {tuple(_CACHE_IO)}")
@@ -538,37 +550,33 @@ def _pages(index: int, k_cache, v_cache=None, k_scale=None, v_scale=None):
         raise ValueError(f"k_cache: shape {tuple(shape)}, expected (num_pages, KV heads, page_size, 128)")
     num, kv, page, _ = shape
     k_stride = 0 if k_cache.is_contiguous() else _row_stride(k_cache, "k_cache", kv * page * 128)
-    v, v_stride = 0, 0
+    v = v_stride = ks = vs = 0
     if v_cache is not None:
         if v_cache.dtype is not dtype or v_cache.shape != shape:
             raise ValueError(f"v_cache: expected {dtype} of shape {tuple(shape)}")
         v_stride = 0 if v_cache.is_contiguous() else _row_stride(v_cache, "v_cache", kv * page * 128)
         v = v_cache.data_ptr()
-    ks = vs = 0
+        if v_cache.get_device() != index:
+            _on(index, v_cache=v_cache)
     if k_scale is not None or v_scale is not None:
         if dtype is not torch.float8_e4m3fn:
             raise ValueError("k_scale, v_scale: only float8_e4m3fn caches have scales")
-        if k_scale is not None:
-            _vector(k_scale, "k_scale", kv, torch.float32)
-            ks = k_scale.data_ptr()
-        if v_scale is not None:
-            _vector(v_scale, "v_scale", kv, torch.float32)
-            vs = v_scale.data_ptr()
-        _on(index, k_scale=k_scale, v_scale=v_scale)
-    if k_cache.get_device() != index or (v_cache is not None and v_cache.get_device() != index):
-        _on(index, k_cache=k_cache, v_cache=v_cache)
-    return _lib.Pages(k_cache.data_ptr(), v, _DT[dtype], num, kv, page, k_stride, v_stride, ks, vs), num, kv
+        ks = 0 if k_scale is None else _vector(k_scale, "k_scale", kv, index, torch.float32)
+        vs = 0 if v_scale is None else _vector(v_scale, "v_scale", kv, index, torch.float32)
+    if k_cache.get_device() != index:
+        _on(index, k_cache=k_cache)
+    return _PAGES.pack(k_cache.data_ptr(), v, _DT[dtype], num, kv, page, k_stride, v_stride, ks, vs), num, kv
 
 
-def _table(index: int, table, lens, B: int):
-    """(row stride, max_pages) of a page table for B requests."""
+def _table(index: int, table, B: int):
+    """(address, row stride, max_pages) of a page table for B requests."""
     shape = table.shape
     if table.dtype is not _I32 or len(shape) != 2 or shape[0] != B:
         raise ValueError(f"table: expected int32 of shape ({B}, max_pages), got {table.dtype} {tuple(shape)}")
-    _vector(lens, "lens", B)
-    if table.get_device() != index or lens.get_device() != index:
-        _on(index, table=table, lens=lens)
-    return (shape[1] if table.is_contiguous() else _row_stride(table, "table", shape[1])), shape[1]
+    if table.get_device() != index:
+        _on(index, table=table)
+    width = shape[1]
+    return table.data_ptr(), (width if table.is_contiguous() else _row_stride(table, "table", width)), width
 
 
 def _page_ws(ws, nbytes: int, dev):
@@ -606,23 +614,24 @@ def page_map(cached: torch.Tensor, added: torch.Tensor, table: torch.Tensor, fre
         with torch.cuda.device(cached.device):
             return page_map(cached, added, table, free_pages, taken, page_size, num_pages, tokens, taken_out, ws)
     dev, index, B, n_free = cached.device, cached.get_device(), cached.shape[0], free_pages.shape[0]
-    stride, max_pages = _table(index, table, cached, B)
-    _vector(added, "added", B)
-    _vector(free_pages, "free_pages", n_free)
-    _vector(taken, "taken", 1)
-    if added.get_device() != index or free_pages.get_device() != index or taken.get_device() != index:
-        _on(index, added=added, free_pages=free_pages, taken=taken)
-    lens, starts, slots, positions, out = torch.empty(2 * (B + tokens + 1), dtype=_I32, device=dev).split_with_sizes(
-        [B, B + 1, tokens, tokens, 1])
+    p_cached, p_added = _vector(cached, "cached", B, index), _vector(added, "added", B, index)
+    p_table, stride, max_pages = _table(index, table, B)
+    p_free, p_taken = _vector(free_pages, "free_pages", n_free, index), _vector(taken, "taken", 1, index)
+    # The outputs, in one allocation.
+    buf = torch.empty(2 * (B + tokens + 1), dtype=_I32, device=dev)
+    lens, starts, slots, positions, out = buf.split_with_sizes([B, B + 1, tokens, tokens, 1])
+    p_lens = buf.data_ptr()
+    p_starts = p_lens + 4 * B
+    p_slots = p_starts + 4 * (B + 1)
+    p_positions = p_slots + 4 * tokens
+    p_out = p_positions + 4 * tokens
     if taken_out is not None:
-        _vector(taken_out, "taken_out", 1)
-        _on(index, taken_out=taken_out)
-        out = taken_out
+        out, p_out = taken_out, _vector(taken_out, "taken_out", 1, index)
     p_ws, n_ws, stream = _page_ws(ws, _STATUS_BYTES, dev)
-    _lib.check(_lib.load().mova_page_map(
-        cached.data_ptr(), added.data_ptr(), B, table.data_ptr(), stride, max_pages, free_pages.data_ptr(), n_free,
-        taken.data_ptr(), page_size, num_pages, tokens, lens.data_ptr(), starts.data_ptr(), slots.data_ptr(),
-        positions.data_ptr(), out.data_ptr(), p_ws, n_ws, stream), "mova_page_map")
+    code = _lib.load().mova_page_map(p_cached, p_added, B, p_table, stride, max_pages, p_free, n_free, p_taken, page_size,
+                                     num_pages, tokens, p_lens, p_starts, p_slots, p_positions, p_out, p_ws, n_ws, stream)
+    if code:
+        _lib.check(code, "mova_page_map")
     return lens, starts, slots, positions, out
 
 
@@ -643,12 +652,14 @@ def page_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: t
     k_stride, v_stride = _row_stride(k, "k", kv * 128), _row_stride(v, "v", kv * 128)
     if v.shape[0] != T:
         raise ValueError(f"v: {v.shape[0]} tokens, expected {T}")
-    _vector(slots, "slots", T)
-    if v.get_device() != index or slots.get_device() != index:
-        _on(index, v=v, slots=slots)
+    p_slots = _vector(slots, "slots", T, index)
+    if v.get_device() != index:
+        _on(index, v=v)
     p_ws, n_ws, stream = _page_ws(ws, _STATUS_BYTES, dev)
-    _lib.check(_lib.load().mova_page_write(k.data_ptr(), v.data_ptr(), _DT[io], k_stride, v_stride, slots.data_ptr(),
-                                           T, ctypes.addressof(p), p_ws, n_ws, stream), "mova_page_write")
+    code = _lib.load().mova_page_write(k.data_ptr(), v.data_ptr(), _DT[io], k_stride, v_stride, p_slots, T, p, p_ws, n_ws,
+                                       stream)
+    if code:
+        _lib.check(code, "mova_page_write")
 
 
 def _bounds(index: int, k_lo, k_hi, want, dtype) -> None:
@@ -670,15 +681,14 @@ def page_bounds(k_cache: torch.Tensor, table: torch.Tensor, cached: torch.Tensor
             return page_bounds(k_cache, table, cached, lens, k_lo, k_hi, ws)
     dev, index, B = k_cache.device, k_cache.get_device(), lens.shape[0]
     p, num, kv = _pages(index, k_cache)
-    stride, max_pages = _table(index, table, lens, B)
-    _vector(cached, "cached", B)
-    if cached.get_device() != index:
-        _on(index, cached=cached)
+    p_table, stride, max_pages = _table(index, table, B)
+    p_cached, p_lens = _vector(cached, "cached", B, index), _vector(lens, "lens", B, index)
     _bounds(index, k_lo, k_hi, (num, kv, 128), k_cache.dtype)
     p_ws, n_ws, stream = _page_ws(ws, _STATUS_BYTES, dev)
-    _lib.check(_lib.load().mova_page_bounds(ctypes.addressof(p), table.data_ptr(), stride, max_pages,
-                                            cached.data_ptr(), lens.data_ptr(), B, k_lo.data_ptr(), k_hi.data_ptr(),
-                                            p_ws, n_ws, stream), "mova_page_bounds")
+    code = _lib.load().mova_page_bounds(p, p_table, stride, max_pages, p_cached, p_lens, B, k_lo.data_ptr(),
+                                        k_hi.data_ptr(), p_ws, n_ws, stream)
+    if code:
+        _lib.check(code, "mova_page_bounds")
 
 
 def page_select(q: torch.Tensor, k_lo: torch.Tensor, k_hi: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
@@ -696,14 +706,15 @@ def page_select(q: torch.Tensor, k_lo: torch.Tensor, k_hi: torch.Tensor, table: 
     _bounds(index, k_lo, k_hi, shape, dtype)
     B, H = _heads(q, "q", _CACHE_IO[dtype])
     q_stride = _row_stride(q, "q", H * 128)
-    stride, max_pages = _table(index, table, lens, B)
+    p_table, stride, max_pages = _table(index, table, B)
+    p_lens = _vector(lens, "lens", B, index)
     picked = torch.empty(B, kv, top, dtype=_I32, device=dev)
-    p = _lib.Pages(0, 0, _DT[dtype], num, kv, page_size, 0, 0, 0, 0)
+    p = _PAGES.pack(0, 0, _DT[dtype], num, kv, page_size, 0, 0, 0, 0)
     p_ws, n_ws, stream = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
-    _lib.check(_lib.load().mova_page_select(q.data_ptr(), _DT[q.dtype], q_stride, H, ctypes.addressof(p),
-                                            k_lo.data_ptr(), k_hi.data_ptr(), table.data_ptr(), stride, max_pages,
-                                            lens.data_ptr(), B, top, picked.data_ptr(), p_ws, n_ws, stream),
-               "mova_page_select")
+    code = _lib.load().mova_page_select(q.data_ptr(), _DT[q.dtype], q_stride, H, p, k_lo.data_ptr(), k_hi.data_ptr(),
+                                        p_table, stride, max_pages, p_lens, B, top, picked.data_ptr(), p_ws, n_ws, stream)
+    if code:
+        _lib.check(code, "mova_page_select")
     return picked
 
 
@@ -722,8 +733,9 @@ def page_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, t
     p, _, kv = _pages(index, k_cache, v_cache, k_scale, v_scale)
     B, H = _heads(q, "q", _CACHE_IO[k_cache.dtype])
     q_stride = _row_stride(q, "q", H * 128)
-    stride, max_pages = _table(index, table, lens, B)
-    p_picked = top = 0
+    p_table, stride, max_pages = _table(index, table, B)
+    p_lens = _vector(lens, "lens", B, index)
+    p_picked = top = p_lse = 0
     if picked is not None:
         if picked.dtype is not _I32 or picked.dim() != 3 or picked.shape[:2] != (B, kv) or not picked.is_contiguous():
             raise ValueError(f"picked: expected contiguous int32 of shape ({B}, {kv}, top), got {picked.dtype} "
@@ -737,12 +749,15 @@ def page_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, t
         raise ValueError(f"out: expected contiguous {q.dtype} of shape {tuple(q.shape)}")
     else:
         _on(index, out=out)
-    lse = torch.empty(B, H, dtype=torch.float32, device=dev) if return_lse else None
+    if return_lse:
+        lse = torch.empty(B, H, dtype=torch.float32, device=dev)
+        p_lse = lse.data_ptr()
     p_ws, n_ws, stream = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
-    _lib.check(_lib.load().mova_page_attend(
-        q.data_ptr(), _DT[q.dtype], q_stride, H, ctypes.addressof(p), table.data_ptr(), stride, max_pages,
-        lens.data_ptr(), B, _RSQRT_128 if scale is None else scale, p_picked, top, out.data_ptr(),
-        lse.data_ptr() if return_lse else None, p_ws, n_ws, stream), "mova_page_attend")
+    code = _lib.load().mova_page_attend(q.data_ptr(), _DT[q.dtype], q_stride, H, p, p_table, stride, max_pages, p_lens, B,
+                                        _RSQRT_128 if scale is None else scale, p_picked, top, out.data_ptr(), p_lse,
+                                        p_ws, n_ws, stream)
+    if code:
+        _lib.check(code, "mova_page_attend")
     return (out, lse) if return_lse else out
 
 

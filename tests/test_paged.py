@@ -290,6 +290,11 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     assert seen == [s["q"].device, "out"]
 
 
+def test_packed_pages_are_the_struct():
+    p = _lib.Pages(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
+    assert bytes(p) == api._PAGES.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
+
+
 # ---- The plain implementations -----------------------------------------------------
 
 def test_e4m3_rounding_agrees_with_torch():
