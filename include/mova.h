@@ -455,7 +455,7 @@ mova_status mova_value_routed_noalloc(const void* x, mova_dtype x_dt, const floa
  *    KV head h / G, G = H / kv_heads from 1 to 16.
  *  - page_size is 16, 32, 64, 128 or 256; at most 4096 requests per call;
  *    num_pages * page_size < 2^31; max_pages * page_size <= 2^30; requests *
- *    max_pages * page_size * kv_heads < 2^34.
+ *    max_pages * page_size * kv_heads < 2^33.
  *  - Types: fp32 pages with fp32 q, k, v and outputs; bf16 pages, or E4M3
  *    pages with one fp32 scale per KV head (value = stored * scale), with
  *    bf16 q, k, v and outputs.  Other pairs: MOVA_ERR_UNSUPPORTED.

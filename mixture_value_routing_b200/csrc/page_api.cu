@@ -83,7 +83,7 @@ mova_status read_table(const mova_pages& p, const int32_t* table, long long tabl
   if (st != MOVA_OK) return st;
   const long long tokens = static_cast<long long>(max_pages) * p.page_size;
   if (tokens > (1LL << 30)) return MOVA_ERR_UNSUPPORTED;
-  if (static_cast<double>(tokens) * B * p.kv_heads >= static_cast<double>(1LL << 34)) return MOVA_ERR_UNSUPPORTED;
+  if (static_cast<double>(tokens) * B * p.kv_heads >= static_cast<double>(1LL << 33)) return MOVA_ERR_UNSUPPORTED;
   if (table_stride == 0) table_stride = max_pages;
   if (table_stride < max_pages || table_stride > (1LL << 40)) return MOVA_ERR_INVALID_ARG;
   if (B > 0 && (!table || !lens || !aligned(table, 4) || !aligned(lens, 4))) return MOVA_ERR_INVALID_ARG;
@@ -99,7 +99,7 @@ PageWs layout(void* base, int B, int max_pages, int kv, int H) {
   w.sb = reinterpret_cast<StatusBlock*>(b);
   o += kStatusBytes;
   w.bad = reinterpret_cast<int32_t*>(b + o);
-  o += align256(kMaxWorkers * sizeof(int32_t));
+  o += align256(kMaxCtas * sizeof(int32_t));
   w.prefix = reinterpret_cast<int32_t*>(b + o);
   o += align256(static_cast<size_t>(B + 1) * sizeof(int32_t));
   // The scores are gone before the attention that follows writes partial results.

@@ -7,22 +7,23 @@
 // operations, G <= 16: far below the tensor cores' rate at any G, so the
 // bytes of K and V bound it and every step below serves the memory stream.
 //
-// Split.  The units of work -- 64 keys (bf16), 128 (E4M3) or 32 (fp32) of one
-// (request, KV head) -- are laid out in one line, request by request and
-// head by head, and each of the resident CTAs takes an equal, contiguous
-// share.  Lengths are known on the device only, so every CTA scans them
-// itself.  A CTA that covers a (request, head) alone writes its output; where
+// Split.  The keys of all rows -- a row is a (request, KV head) -- are laid out
+// in one line of units, row by row, and each of the resident workers takes an
+// equal, contiguous share.  Lengths are known on the device only, so every CTA
+// scans them itself.  A worker that covers a row alone writes its output; where
 // several share one, each leaves a partial result (running maximum, sum, and
 // unnormalised output) and the second kernel joins them in the order of the
-// keys.  A CTA has at most two partial results, its first and its last, so
-// the workspace does not grow with the batch.
+// keys.  A worker has at most two partial results, its first and its last, so
+// the workspace does not grow with the batch.  A worker is a CTA, whose four
+// warps take a tile of each unit (16 keys of bf16, 32 of E4M3, 8 of fp32) and
+// join where a row ends; or, where there are many rows, which may be short, a
+// warp alone, as the joining costs more than a short row.
 //
-// Stream.  Each warp owns every fourth tile of its CTA's units and a ring of
-// kStages 8 KB stages (K and V of one tile) that it fills with 16-byte
-// asynchronous copies, a few tiles ahead and across (request, head)
-// boundaries, so the stream does not stop where a softmax ends.  Page numbers
-// are looked up 32 tiles at a time, one per lane.  Tokens past the end and
-// pages that are none are filled with zeros and their scores set to -inf.
+// Stream.  Each warp has a ring of 8 KB stages (K and V of one tile) that it
+// fills with 16-byte asynchronous copies, one or two tiles ahead and across
+// rows, so the stream does not stop where a softmax ends.  Page numbers are
+// looked up 32 tiles at a time, one per lane.  Tokens past the end and pages
+// that are none are filled with zeros and their scores set to -inf.
 //
 // Mathematics.  bf16: S^T = K q^T and O^T = V^T P^T on mma.m16n8k16, keys (or
 // dimensions) as the 16 rows and query heads as the 8 columns, so that G <= 8
@@ -419,9 +420,18 @@ __device__ __forceinline__ void tile_f32(State<kF32, NT>& st, const float* q, fl
   }
 }
 
-// First unit of worker w of W <= U, U units in all; and the worker of unit u.
-// Every worker has a unit, so every one between a row's first and last
-// leaves a partial result.
+// A worker is a team of kTeam warps, and its unit of work kTeam tiles in a row,
+// one for each warp.  Units that a worker has at least: a lone warp as many as
+// it has in flight, so that a short row is not cut into more parts than its
+// latency repays.
+template <int M, int kTeam> constexpr int kLeast = kTeam > 1 ? 1 : Tile<M>::stages;
+
+// The workers that take part, U units in all; the first unit of worker w of W
+// <= U, and the worker of unit u.  Every worker has a unit, so every one
+// between a row's first and last leaves a partial result.
+template <int M, int kTeam> __device__ __forceinline__ int workers_for(int ctas, int U) {
+  return min(ctas * (kWarps / kTeam), (U + kLeast<M, kTeam> - 1) / kLeast<M, kTeam>);
+}
 __device__ __forceinline__ int first_unit(int w, int W, int U) {
   return static_cast<int>(static_cast<long long>(w) * U / W);
 }
@@ -429,24 +439,33 @@ __device__ __forceinline__ int worker_of(int u, int W, int U) {
   return static_cast<int>((static_cast<long long>(u + 1) * W - 1) / U);
 }
 
-// Dynamic shared memory: the ring, the fp32 queries (NT heads), the prefix.
-template <int M, int NT>
+// Dynamic shared memory: the rings, each worker's fp32 queries (NT heads), the prefix.
+template <int M, int NT, int kTeam>
 __host__ __device__ constexpr size_t attend_smem(int B) {
-  return kRingAlign + kWarps * Tile<M>::stages * kStageBytes + (M == kF32 ? NT * kHeadDim * 4 : 0) + static_cast<size_t>(B + 1) * 4;
+  return kRingAlign + kWarps * Tile<M>::stages * kStageBytes +
+         (M == kF32 ? kWarps / kTeam * NT * kHeadDim * 4 : 0) + static_cast<size_t>(B + 1) * 4;
 }
 
-// Where the warps are joined, head's dimension d lies at d ^ join_swizzle(head):
-// the four heads that a warp stores at once then use different banks.
-__device__ __forceinline__ int join_swizzle(int head) { return ((head >> 1) & 3) << 3; }
+// Where a warp turns its outputs round, head's dimension d lies at
+// d ^ turn_swizzle(head): the four heads that it stores at once use different banks.
+__device__ __forceinline__ int turn_swizzle(int head) { return ((head >> 1) & 3) << 3; }
+
+// Four consecutive outputs of one head.
+template <int M> __device__ __forceinline__ void store_out(void* o, long long at, const float4& v) {
+  if constexpr (M == kF32)
+    *reinterpret_cast<float4*>(static_cast<float*>(o) + at) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+}
 
 // NT: mma column tiles of 8 heads, or fp32 heads.
-template <int M, int NT>
+template <int M, int NT, int kTeam>
 __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs s) {
   using E = typename Tile<M>::E;
   using Out = typename std::conditional<M == kF32, float, __nv_bfloat16>::type;
   constexpr int kKeys = Tile<M>::keys;
+  constexpr int kUnit = kTeam * kKeys;
   constexpr int kGroups = Tile<M>::groups;
-  constexpr int kUnit = kWarps * kKeys;
   constexpr int kStages = Tile<M>::stages;
   constexpr int kRow = kHeadDim * sizeof(E);      // bytes of a key
   constexpr int kChunks = kRow / 16;
@@ -459,9 +478,10 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
   char* smem = smem_raw + ((kRingAlign - (smem_u32(smem_raw) & (kRingAlign - 1))) & (kRingAlign - 1));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = s.G, kv = s.a.kv, B = s.a.B, shift = s.a.shift;
-  float* q_sm = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
-  int* pre = reinterpret_cast<int*>(q_sm + (M == kF32 ? NT * kHeadDim : 0));
-  const int w = blockIdx.x;
+  char* ring_base = smem + warp * (kStages * kStageBytes);
+  float* q_all = reinterpret_cast<float*>(smem + kWarps * kStages * kStageBytes);
+  float* q_sm = q_all + (M == kF32 ? warp / kTeam * NT * kHeadDim : 0);
+  int* pre = reinterpret_cast<int*>(q_all + (M == kF32 ? kWarps / kTeam * NT * kHeadDim : 0));
 
   if (tid == 0) sm_bad = kNoBad;
   pdl_wait();
@@ -472,13 +492,14 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
     return (places_of(s, use) + kUnit - 1) / kUnit;
   });
   const int U = kv * pre[B];
-  if (w == 0)
+  if (blockIdx.x == 0)
     for (int b = tid; b <= B; b += kThreads) s.prefix[b] = pre[b];
-  const int W = min(static_cast<int>(gridDim.x), U);
+  const int w = (blockIdx.x * kWarps + warp) / kTeam, W = workers_for<M, kTeam>(gridDim.x, U);
   const int u0 = w < W ? first_unit(w, W, U) : 0, count = w < W ? first_unit(w + 1, W, U) - u0 : 0;
 
-  // Page lookup of 32 tiles: lane i that of tile `at + i` of this warp.
-  int t_page[kGroups], t_row[kGroups], t_valid[kGroups];
+  // Page lookup of 32 tiles: lane i that of this warp's tile in unit `at + i`,
+  // with the row (request, KV head) that it belongs to.
+  int t_page[kGroups], t_row[kGroups], t_valid[kGroups], t_owner = -1;
   auto look_up = [&](int at) {
     const int i = at + lane;
 #pragma unroll
@@ -489,9 +510,10 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
     const int tiles = pre[b + 1] - pre[b], rem = u - kv * pre[b];
     const int h = rem / tiles;
     const int len = clamp_len(s.a.lens[b], s.a.max_pages, shift);
+    t_owner = b * kv + h;
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
-      const int place = (rem - h * tiles) * kUnit + warp * kKeys + 16 * j;
+      const int place = (rem - h * tiles) * kUnit + warp % kTeam * kKeys + 16 * j;
       const int in = place & ((1 << shift) - 1);
       int page = place >> shift;
       if (s.picked != nullptr) {
@@ -515,7 +537,11 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
       t_valid[j] = valid;
     }
   };
-  const uint32_t ring = smem_u32(smem) + warp * (kStages * kStageBytes);
+  // The query rows of (request, KV head) number `owner`, in elements.
+  auto q_at = [&](int owner) {
+    return (owner / kv) * s.q_stride + static_cast<long long>(owner % kv) * G * kHeadDim;
+  };
+  const uint32_t ring = smem_u32(ring_base);
   const char* k_base = static_cast<const char*>(s.a.k);
   const char* v_base = static_cast<const char*>(s.a.v);
   constexpr int kRowsPer = 32 / kChunks;               // rows of one warp-wide copy
@@ -528,10 +554,21 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
     const int r = x * kRowsPer + lane / kChunks, c = lane % kChunks;
     swz[x] = r * kRow + ((M == kF32 ? c ^ ((r & 1) << 2) : c ^ (r & 7)) << 4);
   }
-  // Starts the copies of tile i (of this warp) into its stage.
+  // Starts the copies of tile i (of this warp) into its stage.  Where a new row
+  // begins, its queries are called into the cache: they are needed with its keys.
+  int ahead = -1;
   auto issue = [&](int i) {
     if ((i & 31) == 0) look_up(i);
     if (i < count) {
+      const int owner = __shfl_sync(0xffffffffu, t_owner, i & 31);
+      if (owner != ahead) {
+        ahead = owner;
+        const int line = lane * 128;
+        if (line < G * kHeadDim * (M == kF32 ? 4 : 2)) {
+          const char* at = static_cast<const char*>(s.q) + q_at(owner) * (M == kF32 ? 4 : 2) + line;
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+        }
+      }
       const int stage = i % kStages;
       const uint32_t dst = ring + stage * kStageBytes;
 #pragma unroll
@@ -578,11 +615,13 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
     for (int i = 0; i < count; ++i) {
       if (fresh) {
         st.clear();
-        const long long at = b * s.q_stride + static_cast<long long>(h) * G * kHeadDim;
+        const long long at = q_at(b * kv + h);
         if constexpr (M == kF32) {
           const float* src = static_cast<const float*>(s.q) + at;
-          for (int x = tid; x < NT * kHeadDim; x += kThreads) q_sm[x] = x < G * kHeadDim ? src[x] : 0.0f;
-          __syncthreads();
+          for (int x = kTeam > 1 ? tid : lane; x < NT * kHeadDim / 4; x += kTeam > 1 ? kThreads : 32)
+            reinterpret_cast<float4*>(q_sm)[x] =
+                4 * x < G * kHeadDim ? reinterpret_cast<const float4*>(src)[x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if constexpr (kTeam > 1) __syncthreads();
         } else {
           const float k_scale = M == kE8 && s.a.k_scale != nullptr ? s.a.k_scale[h] : 1.0f;
           load_query<M, NT>(q, static_cast<const __nv_bfloat16*>(s.q) + at, G, s.scale * kLog2e * k_scale, lane);
@@ -590,27 +629,46 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
         fresh = false;
       }
       cp_wait<kStages - 2>();
-      __syncwarp();
+      __syncwarp();  // the tile (and q_sm) is there; every lane has done with the tile before
       issue(i + kStages - 1);
       const int stage = i % kStages;
       const uint32_t kt = ring + stage * kStageBytes, vt = kt + kStageBytes / 2;
+      char* tile = ring_base + stage * kStageBytes;
       if constexpr (M == kB16) {
         tile_b16<NT>(st, q, kt, vt, sm_valid[warp][stage][0], lane);
       } else if constexpr (M == kE8) {
         tile_e8<NT>(st, q, kt, vt, sm_valid[warp][stage][0], sm_valid[warp][stage][1], lane);
       } else {
-        const char* p = smem + (warp * kStages + stage) * kStageBytes;
-        tile_f32<NT>(st, q_sm, s.scale * kLog2e, p, p + kStageBytes / 2, sm_valid[warp][stage][0], lane);
+        tile_f32<NT>(st, q_sm, s.scale * kLog2e, tile, tile + kStageBytes / 2, sm_valid[warp][stage][0], lane);
       }
       const bool row_end = t + 1 == tiles;
       if (row_end || i + 1 == count) {
-        // Join the four warps: maxima, sums and outputs through shared memory.  A
-        // warp's outputs (at most 16 heads x 512 bytes) go where the tile it has
-        // just used was: the next copies into that stage are started after this.
-        const int g = lane >> 2, t4 = lane & 3;
-        const int join0 = stage * kStageBytes / 4;
-        float* join = reinterpret_cast<float*>(smem) + join0;  // warp x's at x * kStages * kStageBytes / 4
-        constexpr int kJoinWarp = kStages * kStageBytes / 4;
+        // The row is done, or what this worker has of it.  Each warp lays its
+        // outputs where the tile it has just used was (at most 16 heads x 512
+        // bytes; the next copies into that stage start later), to be read back by
+        // head: by a warp alone four dimensions a lane, by a team joined.
+        const bool done = whole && row_end;
+        float* part = s.part + (static_cast<size_t>(w) * 2 + (whole ? 1 : 0)) * (G * kPartRow);
+        const long long row = static_cast<long long>(b) * kv + h;
+        const float v_scale = M == kE8 && s.a.v_scale != nullptr ? s.a.v_scale[h] : 1.0f;
+        float* turn = reinterpret_cast<float*>(tile);
+        auto note = [&](int head, float m, float l) {
+          if (done) {
+            if (s.lse != nullptr) s.lse[row * G + head] = (m + log2f(l)) * kLn2;
+          } else {
+            part[G * kHeadDim + head] = m, part[G * (kHeadDim + 1) + head] = l;
+          }
+        };
+        // Warp alone: lane l puts dimensions 4 l .. 4 l + 3.
+        auto put = [&](int head, float m, float l, float4 v) {
+          const float f = done ? v_scale / l : v_scale;
+          v = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+          if (done)
+            store_out<M>(s.o, (row * G + head) * kHeadDim + 4 * lane, v);
+          else
+            *reinterpret_cast<float4*>(part + head * kHeadDim + 4 * lane) = v;
+          if (lane == 0) note(head, m, l);
+        };
         __syncwarp();  // every lane has read the tile
         if constexpr (M == kF32) {
 #pragma unroll
@@ -618,13 +676,18 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
             float l = st.l[n][0];  // the four lanes of a key hold the same
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            const float4 v = make_float4(st.o[0][n][0], st.o[0][n][1], st.o[0][n][2], st.o[0][n][3]);
             if (n < G) {
-              if (lane == 0) sm_m[warp][n] = st.m[n][0], sm_l[warp][n] = l;
-              *reinterpret_cast<float4*>(&join[warp * kJoinWarp + n * kHeadDim + ((4 * lane) ^ join_swizzle(n))]) =
-                  make_float4(st.o[0][n][0], st.o[0][n][1], st.o[0][n][2], st.o[0][n][3]);
+              if constexpr (kTeam == 1) {
+                put(n, st.m[n][0], l, v);
+              } else {
+                if (lane == 0) sm_m[warp][n] = st.m[n][0], sm_l[warp][n] = l;
+                *reinterpret_cast<float4*>(&turn[n * kHeadDim + ((4 * lane) ^ turn_swizzle(n))]) = v;
+              }
             }
           }
         } else {
+          const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -635,46 +698,53 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
               const int head = n * 8 + 2 * t4 + c;
               if (head < G) {
                 if (g == 0) sm_m[warp][head] = st.m[n][c], sm_l[warp][head] = l;
-                float* row = &join[warp * kJoinWarp + head * kHeadDim];
-                const int swz = join_swizzle(head);
+                float* to = &turn[head * kHeadDim];
+                const int z = turn_swizzle(head);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                   if constexpr (M == kE8) {
-                    *reinterpret_cast<float2*>(&row[(16 * x + 2 * g) ^ swz]) = make_float2(st.o[x][n][c], st.o[x][n][c + 2]);
+                    *reinterpret_cast<float2*>(&to[(16 * x + 2 * g) ^ z]) = make_float2(st.o[x][n][c], st.o[x][n][c + 2]);
                   } else {
-                    row[(16 * x + g) ^ swz] = st.o[x][n][c];
-                    row[(16 * x + g + 8) ^ swz] = st.o[x][n][c + 2];
+                    to[(16 * x + g) ^ z] = st.o[x][n][c];
+                    to[(16 * x + g + 8) ^ z] = st.o[x][n][c + 2];
                   }
                 }
               }
             }
-        }
-        __syncthreads();
-        const float v_scale = M == kE8 && s.a.v_scale != nullptr ? s.a.v_scale[h] : 1.0f;
-        const bool done = whole && row_end;
-        float* part = s.part + static_cast<size_t>(w * 2 + (whole ? 1 : 0)) * (G * kPartRow);
-        for (int head = 0; head < G; ++head) {
-          float m = -INFINITY;
-#pragma unroll
-          for (int x = 0; x < kWarps; ++x) m = fmaxf(m, sm_m[x][head]);
-          float l = 0.0f, o = 0.0f;
-#pragma unroll
-          for (int x = 0; x < kWarps; ++x) {
-            const float f = ex2(sm_m[x][head] - ref_of(m));
-            l = fmaf(sm_l[x][head], f, l);
-            o = fmaf(join[x * kJoinWarp + head * kHeadDim + (tid ^ join_swizzle(head))], f, o);
-          }
-          o *= v_scale;
-          if (done) {
-            const long long at = (static_cast<long long>(b) * kv + h) * G + head;
-            static_cast<Out*>(s.o)[at * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : o / l);
-            if (s.lse != nullptr && tid == 0) s.lse[at] = (m + log2f(l)) * kLn2;
-          } else {
-            part[head * kHeadDim + tid] = o;
-            if (tid == 0) part[G * kHeadDim + head] = m, part[G * (kHeadDim + 1) + head] = l;
+          if constexpr (kTeam == 1) {
+            __syncwarp();
+            for (int head = 0; head < G; ++head)
+              put(head, sm_m[warp][head], sm_l[warp][head],
+                  *reinterpret_cast<const float4*>(&turn[head * kHeadDim + ((4 * lane) ^ turn_swizzle(head))]));
           }
         }
-        __syncthreads();
+        if constexpr (kTeam == 1) {
+          __syncwarp();  // q_sm, sm_m and sm_l are free again
+        } else {
+          // A thread joins one dimension of the team's outputs.
+          const float* all = reinterpret_cast<const float*>(smem + stage * kStageBytes);
+          constexpr int kNext = kStages * kStageBytes / 4;  // from one warp's stage to the next's
+          __syncthreads();
+          for (int head = 0; head < G; ++head) {
+            float m = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < kTeam; ++x) m = fmaxf(m, sm_m[x][head]);
+            float l = 0.0f, o = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kTeam; ++x) {
+              const float f = ex2(sm_m[x][head] - ref_of(m));
+              l = fmaf(sm_l[x][head], f, l);
+              o = fmaf(all[x * kNext + head * kHeadDim + (tid ^ turn_swizzle(head))], f, o);
+            }
+            o = l == 0.0f ? 0.0f : o * v_scale;
+            if (done)
+              static_cast<Out*>(s.o)[(row * G + head) * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : o / l);
+            else
+              part[head * kHeadDim + tid] = o;
+            if (tid == 0) note(head, m, l);
+          }
+          __syncthreads();
+        }
         fresh = whole = true;
         t = -1;
         if (row_end && i + 1 < count) {
@@ -693,7 +763,7 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
   // kernel a third of its rate (118 us against 83 for 463 MB of E4M3 pages).
   pdl_trigger();
   __syncthreads();
-  if (tid == 0) s.bad[w] = sm_bad;
+  if (tid == 0) s.bad[blockIdx.x] = sm_bad;
 }
 
 // Joins the partial results of each (request, KV head) that several workers
@@ -702,9 +772,9 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
 // maxima, sums and outputs at once.  kSplit = 1: a CTA holds a warp for each
 // head; otherwise kSplit warps share the one head of a CTA, warp g taking
 // every kSplit-th four parts from the g-th, and are joined at the end.
-template <int M, int kSplit>
+template <int M, int kTeam, int kSplit>
 __global__ void __launch_bounds__(kSplit > 1 ? 32 * kSplit : 32 * kMaxGroup)
-page_join_kernel(const AttendArgs s, int workers, StatusBlock* sb) {
+page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
   constexpr int kAhead = 4;
   __shared__ float4 sm_o[kSplit][kSplit > 1 ? 32 : 1];
   __shared__ float sm_m[kSplit], sm_l[kSplit];
@@ -717,7 +787,7 @@ page_join_kernel(const AttendArgs s, int workers, StatusBlock* sb) {
   const int p0 = s.prefix[b], tiles = s.prefix[b + 1] - p0, U = kv * s.prefix[B];
   if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
     int bad = kNoBad;
-    for (int i = lane; i < workers; i += 32) bad = min(bad, s.bad[i]);
+    for (int i = lane; i < ctas; i += 32) bad = min(bad, s.bad[i]);
     bad = __reduce_min_sync(0xffffffffu, bad);
     if (lane == 0) {
       sb->code = bad == kNoBad ? MOVA_OK : MOVA_ERR_DEVICE_CHECK;
@@ -725,20 +795,15 @@ page_join_kernel(const AttendArgs s, int workers, StatusBlock* sb) {
     }
   }
   const long long at = static_cast<long long>(blockIdx.x) * G + head;
-  auto write = [&](float4 v, float lse) {
-    if constexpr (M == kF32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(s.o) + at * kHeadDim + 4 * lane) = v;
-    } else {
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(s.o) + at * kHeadDim + 4 * lane) =
-          make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-    }
+  auto write = [&](const float4& v, float lse) {
+    store_out<M>(s.o, at * kHeadDim + 4 * lane, v);
     if (s.lse != nullptr && lane == 0) s.lse[at] = lse;
   };
   if (tiles == 0) {
     if (group == 0) write(make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY);
     return;
   }
-  const int W = min(workers, U);
+  const int W = workers_for<M, kTeam>(ctas, U);
   const int u0 = kv * p0 + h * tiles;
   const int w0 = worker_of(u0, W, U), parts = worker_of(u0 + tiles - 1, W, U) - w0 + 1;
   if (parts == 1) return;
@@ -793,34 +858,53 @@ page_join_kernel(const AttendArgs s, int workers, StatusBlock* sb) {
         (m + log2f(l)) * kLn2);
 }
 
-template <int M, int NT>
+template <int M, int NT, int kTeam>
 cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
-  auto kern = page_attend_kernel<M, NT>;
+  auto kern = page_attend_kernel<M, NT, kTeam>;
   static bool done[64] = {false};
-  cudaError_t err = prepare_kernel(kern, attend_smem<M, NT>(kMaxRequests), done);
+  cudaError_t err = prepare_kernel(kern, attend_smem<M, NT, kTeam>(kMaxRequests), done);
   if (err != cudaSuccess) return err;
-  const size_t smem = attend_smem<M, NT>(s.a.B);
-  const int per_sm = static_cast<int>(std::min<size_t>(3, (227 * 1024) / (smem + 2048)));
-  const long long most = static_cast<long long>(s.a.B) * s.a.kv *
-                         (((static_cast<long long>(s.a.max_pages) << s.a.shift) + kWarps * Tile<M>::keys - 1) /
-                          (kWarps * Tile<M>::keys));
-  long long W = static_cast<long long>(sm_count()) * per_sm;
-  if (W > kMaxWorkers) W = kMaxWorkers;
-  if (W > most) W = most < 1 ? 1 : most;
-  err = launch_pdl(kern, dim3(static_cast<unsigned>(W)), dim3(kThreads), smem, stream, s);
+  const size_t smem = attend_smem<M, NT, kTeam>(s.a.B);
+  // CTAs an SM holds at once, by shared memory and registers; all are resident,
+  // as each takes an equal share.  More than three gain nothing.
+  static const int regs = [] {
+    cudaFuncAttributes at{};
+    return cudaFuncGetAttributes(&at, page_attend_kernel<M, NT, kTeam>) == cudaSuccess && at.numRegs > 0 ? at.numRegs
+                                                                                                      : 255;
+  }();
+  const int by_regs = 65536 / (((regs + 7) & ~7) * kThreads);
+  const int per_sm = std::max(1, std::min({3, by_regs, static_cast<int>((227 * 1024) / (smem + 2048))}));
+  constexpr int kCta = kWarps * kLeast<M, kTeam> * Tile<M>::keys;  // tokens that keep a CTA busy
+  const long long tokens = s.picked == nullptr ? static_cast<long long>(s.a.max_pages) << s.a.shift
+                                               : static_cast<long long>(std::min(s.top, s.a.max_pages)) << s.a.shift;
+  const long long most = static_cast<long long>(s.a.B) * s.a.kv * ((tokens + kCta - 1) / kCta);
+  const int ctas = static_cast<int>(std::max(1LL, std::min({static_cast<long long>(sm_count()) * per_sm, most,
+                                                             static_cast<long long>(kMaxCtas)})));
+  err = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, s);
   if (err != cudaSuccess) return err;
   // Few rows have many parts each, and leave SMs free: a CTA per head.
   const int rows = s.a.B * s.a.kv;
   if (static_cast<long long>(rows) * s.G <= 4LL * sm_count()) {
     static bool split_done[64] = {false};
-    err = prepare_kernel(page_join_kernel<M, 4>, 0, split_done);
+    err = prepare_kernel(page_join_kernel<M, kTeam, 4>, 0, split_done);
     if (err != cudaSuccess) return err;
-    return launch_pdl(page_join_kernel<M, 4>, dim3(rows, s.G), dim3(32 * 4), 0, stream, s, static_cast<int>(W), sb);
+    return launch_pdl(page_join_kernel<M, kTeam, 4>, dim3(rows, s.G), dim3(32 * 4), 0, stream, s, ctas, sb);
   }
   static bool join_done[64] = {false};
-  err = prepare_kernel(page_join_kernel<M, 1>, 0, join_done);
+  err = prepare_kernel(page_join_kernel<M, kTeam, 1>, 0, join_done);
   if (err != cudaSuccess) return err;
-  return launch_pdl(page_join_kernel<M, 1>, dim3(rows), dim3(32 * s.G), 0, stream, s, static_cast<int>(W), sb);
+  return launch_pdl(page_join_kernel<M, kTeam, 1>, dim3(rows), dim3(32 * s.G), 0, stream, s, ctas, sb);
+}
+
+// Rows from which warps work alone.  Measured on bf16: 8192 rows of 100 tokens
+// 135 us alone, 212 in teams; 512 rows of 4096 171 and 169; 64 rows to 500
+// 13.2 and 7.7.
+constexpr int kAloneRows = 1024;
+
+template <int M, int NT>
+cudaError_t launch_attend(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
+  return static_cast<long long>(s.a.B) * s.a.kv >= kAloneRows ? launch_attend_t<M, NT, 1>(s, sb, stream)
+                                                              : launch_attend_t<M, NT, kWarps>(s, sb, stream);
 }
 
 }  // namespace
@@ -830,16 +914,16 @@ cudaError_t launch_page_attend(const void* q, long long q_stride, int G, const P
                                cudaStream_t stream) {
   const AttendArgs s{a, q, q_stride, G, scale, picked, top, o, lse, ws.bad, ws.prefix, ws.part};
   if (dt == MOVA_F32) {
-    if (G <= 4) return launch_attend_t<kF32, 4>(s, ws.sb, stream);
-    if (G <= 8) return launch_attend_t<kF32, 8>(s, ws.sb, stream);
-    return launch_attend_t<kF32, 16>(s, ws.sb, stream);
+    if (G <= 4) return launch_attend<kF32, 4>(s, ws.sb, stream);
+    if (G <= 8) return launch_attend<kF32, 8>(s, ws.sb, stream);
+    return launch_attend<kF32, 16>(s, ws.sb, stream);
   }
   if (dt == MOVA_BF16) {
-    if (G <= 8) return launch_attend_t<kB16, 1>(s, ws.sb, stream);
-    return launch_attend_t<kB16, 2>(s, ws.sb, stream);
+    if (G <= 8) return launch_attend<kB16, 1>(s, ws.sb, stream);
+    return launch_attend<kB16, 2>(s, ws.sb, stream);
   }
-  if (G <= 8) return launch_attend_t<kE8, 1>(s, ws.sb, stream);
-  return launch_attend_t<kE8, 2>(s, ws.sb, stream);
+  if (G <= 8) return launch_attend<kE8, 1>(s, ws.sb, stream);
+  return launch_attend<kE8, 2>(s, ws.sb, stream);
 }
 
 }  // namespace mova

@@ -525,7 +525,7 @@ cudaError_t launch_page_select(const void* q, long long q_stride, int G, const P
   const SelectArgs s{a, q, q_stride, G, top, lo, hi, ws.keys, ws.bad, picked};
   const long long most = (static_cast<long long>(a.B) * a.kv * a.max_pages + kScoreWarps - 1) / kScoreWarps;
   long long ctas = static_cast<long long>(sm_count()) * score_per_sm(G <= 8 ? 1 : 2);
-  if (ctas > kMaxWorkers) ctas = kMaxWorkers;
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
   if (ctas > most) ctas = most < 1 ? 1 : most;
   const int n = static_cast<int>(ctas);
   cudaError_t err;

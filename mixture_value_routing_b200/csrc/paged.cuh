@@ -13,7 +13,8 @@ namespace mova {
 constexpr int kHeadDim = 128;
 constexpr int kMaxRequests = 4096;
 constexpr int kMaxGroup = 16;    // query heads per KV head
-constexpr int kMaxWorkers = 640;  // CTAs of one attention call
+constexpr int kMaxCtas = 592;    // of an attention or score kernel
+constexpr int kMaxWorkers = kMaxCtas * 4;  // warps of an attention kernel
 constexpr int kNoBad = 0x7fffffff;
 // Floats of a partial result per query head: 128 outputs, a maximum and a sum,
 // and two that keep every partial result 16-byte aligned.  The outputs of the
@@ -23,8 +24,8 @@ constexpr int kPartRow = kHeadDim + 4;
 // Parts of the workspace.  `part` holds two partial results per worker.
 struct PageWs {
   StatusBlock* sb;
-  int32_t* bad;     // (kMaxWorkers + 1) first bad request seen by each worker (kNoBad: none)
-  int32_t* prefix;  // (B + 1) units of work before each request
+  int32_t* bad;     // (kMaxCtas) first bad request seen by each CTA (kNoBad: none)
+  int32_t* prefix;  // (B + 1) tiles of one KV head before each request
   float* part;
   unsigned long long* keys;  // select: (B, kv_heads, max_pages) sortable scores
   size_t bytes;
