@@ -23,28 +23,58 @@ namespace {
 
 constexpr int kWriteSmall = 1024;  // CTAs of 512 threads from this many tokens on, 256 below
 
-template <typename In> constexpr int per_chunk() { return 16 / sizeof(In); }
-
-__device__ __forceinline__ uint8_t to_e4m3(float x, float scale) {
-  const float y = __fdiv_rn(x, scale);
-  return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+// x / scale as IEEE division rounds it, from r, the rounded reciprocal of scale:
+// a quotient and one correction by its exact remainder (P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990, theorem on division), for |x| < 2^60 and scale from 2^-60 to 2^40.
+// Signs of zeros come out as the division's; quotients too small for the
+// theorem are 0 in E4M3 either way.
+__device__ __forceinline__ float quotient(float x, float scale, float r) {
+  const float q = x * r;
+  return fmaf(-fmaf(q, scale, -x), r, q);
 }
 
-// Stores one 16-byte input chunk at element `at` of the cache.
-__device__ __forceinline__ void store_chunk(float* cache, long long at, const uint4& x, float) {
-  __stcs(reinterpret_cast<uint4*>(cache + at), x);
-}
-__device__ __forceinline__ void store_chunk(__nv_bfloat16* cache, long long at, const uint4& x, float) {
-  __stcs(reinterpret_cast<uint4*>(cache + at), x);
-}
-__device__ __forceinline__ void store_chunk(uint8_t* cache, long long at, const uint4& x, float scale) {
-  const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&x);
-  uint32_t out[2] = {0u, 0u};
+// One unit of a thread: the 16-byte loads whose elements fill 16 bytes of the cache.
+template <typename In, typename Out> struct Unit {
+  static constexpr int kPer = 16 / sizeof(Out);             // elements
+  static constexpr int kLoads = sizeof(In) / sizeof(Out);   // 16-byte loads
+  uint4 x[kLoads];
+  __device__ __forceinline__ void load(const In* p) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    out[i >> 2] |= static_cast<uint32_t>(to_e4m3(__bfloat162float(e[i]), scale)) << (8 * (i & 3));
-  __stcs(reinterpret_cast<uint2*>(cache + at), make_uint2(out[0], out[1]));
-}
+    for (int i = 0; i < kLoads; ++i) x[i] = ld_stream_u4(p + i * (16 / sizeof(In)));
+  }
+  __device__ __forceinline__ void store(Out* p, float scale) const {
+    if constexpr (sizeof(Out) > 1)
+      __stcs(reinterpret_cast<uint4*>(p), x[0]);
+    else
+      __stcs(reinterpret_cast<uint4*>(p), quantised(scale));
+  }
+  // 16 bf16 elements over the scale, as E4M3.
+  __device__ __forceinline__ uint4 quantised(float scale) const {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    uint32_t big = scale > 0x1p-60f && scale < 0x1p40f ? 0u : 1u;  // outside quotient()'s range
+#pragma unroll
+    for (int i = 0; i < 8; ++i) big |= ((w[i] & 0x7f807f80u) + 0x22802280u) & 0x80008000u;  // exponents from 60 on
+    const float r = __frcp_rn(scale);
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+      out[i] = __nv_cvt_float2_to_fp8x2(make_float2(quotient(lo, scale, r), quotient(hi, scale, r)), __NV_SATFINITE,
+                                        __NV_E4M3);
+    }
+    if (big != 0u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xffff0000u);
+        out[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale)), __NV_SATFINITE,
+                                          __NV_E4M3);
+      }
+    }
+    return make_uint4(out[0] | (out[1] << 16), out[2] | (out[3] << 16), out[4] | (out[5] << 16),
+                      out[6] | (out[7] << 16));
+  }
+};
 
 template <typename In, typename Out, int kThreads>
 __global__ void __launch_bounds__(kThreads)
@@ -52,8 +82,9 @@ page_write_kernel(const In* __restrict__ k, const In* __restrict__ v, long long 
                   const int32_t* __restrict__ slots, int T, Out* __restrict__ kc, Out* __restrict__ vc,
                   long long kp_stride, long long vp_stride, const float* k_scale, const float* v_scale, int kv,
                   int shift, int num_slots, int lanes, StatusBlock* sb) {
-  constexpr int kPer = per_chunk<In>();
-  constexpr int kUnroll = 4;
+  using U = Unit<In, Out>;
+  constexpr int kPer = U::kPer;
+  constexpr int kUnroll = 4 / U::kLoads;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
@@ -76,7 +107,7 @@ page_write_kernel(const In* __restrict__ k, const In* __restrict__ v, long long 
     }
     return;
   }
-  // `lanes` (16 or 32) threads per (token, keys or values).
+  // `lanes` (8, 16 or 32) threads per (token, keys or values).
   const long long unit = (static_cast<long long>(blockIdx.x) * kThreads + tid) / lanes;
   const int lane = tid % lanes;
   const int t = static_cast<int>(unit >> 1);
@@ -92,11 +123,16 @@ page_write_kernel(const In* __restrict__ k, const In* __restrict__ v, long long 
       ok ? (slot >> shift) * (is_v ? vp_stride : kp_stride) + static_cast<long long>(slot & ((1 << shift) - 1)) * kHeadDim
          : 0;
   for (int c0 = lane; c0 < chunks; c0 += lanes * kUnroll) {
-    uint4 x[kUnroll];
+    U x[kUnroll];
+    float f[kUnroll];
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int c = c0 + i * lanes;
-      if (c < chunks) x[i] = ld_stream_u4(src + c * kPer);
+      f[i] = 1.0f;
+      if (c < chunks) {
+        x[i].load(src + c * kPer);
+        if (sizeof(Out) == 1 && scale != nullptr) f[i] = scale[c / (kHeadDim / kPer)];
+      }
     }
     if (!ok) return;
 #pragma unroll
@@ -104,8 +140,7 @@ page_write_kernel(const In* __restrict__ k, const In* __restrict__ v, long long 
       const int c = c0 + i * lanes;
       if (c < chunks) {
         const int h = c / (kHeadDim / kPer), d = (c % (kHeadDim / kPer)) * kPer;
-        const float s = scale == nullptr ? 1.0f : scale[h];
-        store_chunk(cache, base + (static_cast<long long>(h) << shift) * kHeadDim + d, x[i], s);
+        x[i].store(cache + base + (static_cast<long long>(h) << shift) * kHeadDim + d, f[i]);
       }
     }
   }
@@ -114,7 +149,8 @@ page_write_kernel(const In* __restrict__ k, const In* __restrict__ v, long long 
 template <typename In, typename Out, int kThreads>
 cudaError_t launch_write_t(const void* k, const void* v, long long k_stride, long long v_stride, const int32_t* slots,
                            int T, const mova_pages& p, int shift, StatusBlock* sb, cudaStream_t stream) {
-  const int lanes = p.kv_heads * (kHeadDim / per_chunk<In>()) >= 32 ? 32 : 16;
+  const int units = p.kv_heads * (kHeadDim / Unit<In, Out>::kPer);
+  const int lanes = units >= 32 ? 32 : units >= 16 ? 16 : 8;
   const long long blocks = (2LL * T * lanes + kThreads - 1) / kThreads;
   return launch_pdl(page_write_kernel<In, Out, kThreads>, dim3(static_cast<unsigned>(blocks + 1)), dim3(kThreads), 0,
                     stream, static_cast<const In*>(k), static_cast<const In*>(v), k_stride, v_stride, slots, T,
@@ -140,7 +176,7 @@ __device__ __forceinline__ uint32_t as_u32(__half2 v) { return *reinterpret_cast
 template <typename T> __device__ __forceinline__ T from_u32(uint32_t v) { return *reinterpret_cast<T*>(&v); }
 
 // Bounds of one 16-byte chunk of a key: kWords 32-bit words of packed fp32,
-// bf16 or (for E4M3, exactly) fp16.
+// bf16 or (for E4M3, exactly) fp16.  store: the words that a lane keeps.
 template <typename E> struct Range;
 template <> struct Range<float> {
   static constexpr int kWords = 4;
@@ -155,7 +191,9 @@ template <> struct Range<float> {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
     return __float_as_uint(r);
   }
-  static __device__ __forceinline__ uint4 store(const uint32_t (&w)[4]) { return make_uint4(w[0], w[1], w[2], w[3]); }
+  static __device__ __forceinline__ void store(float* p, const uint32_t (&w)[4]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 };
 template <> struct Range<__nv_bfloat16> {
   static constexpr int kWords = 4;
@@ -166,7 +204,9 @@ template <> struct Range<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t greatest(uint32_t a, uint32_t b) {
     return as_u32(__hmax2_nan(from_u32<__nv_bfloat162>(a), from_u32<__nv_bfloat162>(b)));
   }
-  static __device__ __forceinline__ uint4 store(const uint32_t (&w)[4]) { return make_uint4(w[0], w[1], w[2], w[3]); }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const uint32_t (&w)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
 };
 template <> struct Range<uint8_t> {
   static constexpr int kWords = 8;
@@ -182,15 +222,10 @@ template <> struct Range<uint8_t> {
   static __device__ __forceinline__ uint32_t greatest(uint32_t a, uint32_t b) {
     return as_u32(__hmax2_nan(from_u32<__half2>(a), from_u32<__half2>(b)));
   }
-  static __device__ __forceinline__ uint4 store(const uint32_t (&w)[8]) {
-    uint32_t out[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(from_u32<__half2_raw>(w[2 * i]), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(from_u32<__half2_raw>(w[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-      out[i] = lo | (hi << 16);
-    }
-    return make_uint4(out[0], out[1], out[2], out[3]);
+  static __device__ __forceinline__ void store(uint8_t* p, const uint32_t (&w)[8]) {
+    const uint32_t a = __nv_cvt_halfraw2_to_fp8x2(from_u32<__half2_raw>(w[0]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_halfraw2_to_fp8x2(from_u32<__half2_raw>(w[1]), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint32_t*>(p) = a | (b << 16);
   }
 };
 
@@ -202,9 +237,14 @@ page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __re
   constexpr int kPer = 16 / sizeof(E);
   constexpr int kCols = kHeadDim / kPer;  // 16-byte chunks of a key
   constexpr int kRows = 32 / kCols;       // keys of one warp-wide load
-  constexpr int kLoads = 16 / kRows;      // of 16 keys, in flight at once
+#ifndef TAKE8
+#define TAKE8 16
+#endif
+  constexpr int kTake = sizeof(E) == 1 ? TAKE8 : 16;  // keys of a warp, if the page has as many for it
+  constexpr int kLoads = 16 / kRows;
   constexpr int kWarps = kBoundThreads / 32;
-  __shared__ uint32_t red[2][kWarps][2][R::kWords][kCols];
+  constexpr int kKept = R::kWords / kRows;  // words of a lane once the warp's rows are joined
+  __shared__ uint32_t red[2][kWarps][2][kKept][32];
   extern __shared__ int pre[];
   __shared__ int bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -241,11 +281,15 @@ page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __re
     }
     return;
   }
-  // A warp reads 16 keys of one (page, head), or of a long page a quarter, so
+  // A warp reads kTake keys of one (page, head), or of a long page a quarter, so
   // that a CTA takes whole pages: `share` warps each, 4 / share at a time.
-  const int share = min(kWarps, (1 << a.shift) >> 4), rows = (1 << a.shift) / share;
+  const int share = max(1, min(kWarps, (1 << a.shift) / kTake)), rows = (1 << a.shift) / share;
   const int part = warp % share, lane_pair = warp / share, pairs = kWarps / share;
   const int col = lane % kCols, row0 = lane / kCols;
+  // First of the elements of the chunk whose bounds this lane comes to hold.
+  int kept0 = 0;
+#pragma unroll
+  for (int o = kCols, n = kPer / 2; o < 32; o <<= 1, n /= 2) kept0 += lane & o ? n : 0;
   const int work = items * a.kv, CTAs = gridDim.x - 1;  // work: below 2^30, as the entry point has checked
   const int x0 = static_cast<int>(static_cast<long long>(blockIdx.x) * work / CTAs);
   const int x1 = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * work / CTAs);
@@ -262,7 +306,9 @@ page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __re
     if (page >= 0) {
       const E* src = static_cast<const E*>(a.k) + page * a.k_stride +
                      ((static_cast<long long>(h) << a.shift) + part * rows + row0) * kHeadDim + col * kPer;
-      for (int r = 0; r < rows; r += kRows * kLoads) {
+      bool first = true;
+#pragma unroll 4
+      for (int r = 0; r < rows; r += 16) {
         uint4 raw[kLoads];
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) raw[y] = ld_stream_u4(src + (r + y * kRows) * kHeadDim);
@@ -272,40 +318,47 @@ page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __re
           R::load(raw[y], v);
 #pragma unroll
           for (int j = 0; j < R::kWords; ++j) {
-            l[j] = y == 0 && r == 0 ? v[j] : R::least(l[j], v[j]);
-            u[j] = y == 0 && r == 0 ? v[j] : R::greatest(u[j], v[j]);
+            l[j] = y == 0 && first ? v[j] : R::least(l[j], v[j]);
+            u[j] = y == 0 && first ? v[j] : R::greatest(u[j], v[j]);
           }
         }
+        first = false;
       }
+      // Joins the kRows keys that a load holds: a lane hands on half its words and
+      // keeps the other half, so each ends with kKept words of its chunk.
 #pragma unroll
-      for (int o = kCols; o < 32; o <<= 1)
+      for (int o = kCols, n = R::kWords / 2; o < 32; o <<= 1, n /= 2) {
+        const bool upper = lane & o;
 #pragma unroll
-        for (int j = 0; j < R::kWords; ++j) {
-          l[j] = R::least(l[j], __shfl_xor_sync(0xffffffffu, l[j], o));
-          u[j] = R::greatest(u[j], __shfl_xor_sync(0xffffffffu, u[j], o));
+        for (int j = 0; j < n; ++j) {
+          const uint32_t lo_give = upper ? l[j] : l[j + n], lo_keep = upper ? l[j + n] : l[j];
+          const uint32_t hi_give = upper ? u[j] : u[j + n], hi_keep = upper ? u[j + n] : u[j];
+          l[j] = R::least(lo_keep, __shfl_xor_sync(0xffffffffu, lo_give, o));
+          u[j] = R::greatest(hi_keep, __shfl_xor_sync(0xffffffffu, hi_give, o));
         }
+      }
     }
     const int writer = i / pairs % share;  // the warps of a page take turns
     if (share > 1) {
       // One barrier a round: the other buffer is read until the next one.
-      if (page >= 0 && lane < kCols && part != writer) {
+      if (page >= 0 && part != writer) {
 #pragma unroll
-        for (int j = 0; j < R::kWords; ++j) red[buf][warp][0][j][lane] = l[j], red[buf][warp][1][j][lane] = u[j];
+        for (int j = 0; j < kKept; ++j) red[buf][warp][0][j][lane] = l[j], red[buf][warp][1][j][lane] = u[j];
       }
       __syncthreads();
     }
-    if (page >= 0 && lane < kCols && part == writer) {
+    if (page >= 0 && part == writer) {
       for (int y = 1; y < share; ++y) {
         const int from = lane_pair * share + (part + y) % share;
 #pragma unroll
-        for (int j = 0; j < R::kWords; ++j) {
+        for (int j = 0; j < kKept; ++j) {
           l[j] = R::least(l[j], red[buf][from][0][j][lane]);
           u[j] = R::greatest(u[j], red[buf][from][1][j][lane]);
         }
       }
-      const long long out = (static_cast<long long>(page) * a.kv + h) * kHeadDim + col * kPer;
-      *reinterpret_cast<uint4*>(lo + out) = R::store(l);
-      *reinterpret_cast<uint4*>(hi + out) = R::store(u);
+      const long long out = (static_cast<long long>(page) * a.kv + h) * kHeadDim + col * kPer + kept0;
+      R::store(lo + out, l);
+      R::store(hi + out, u);
     }
   }
 }

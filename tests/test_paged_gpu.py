@@ -162,6 +162,28 @@ def test_write(api, dtype, T, kv, page):
     check_write(api, dtype, T, kv, page, seed=T, combined=T % 2 == 1)
 
 
+@pytest.mark.parametrize("low,high", [(-126, 126), (-12, 3)])
+def test_write_e4m3_divides_exactly(api, low, high):
+    """Every bf16 number over scales of many sizes: the stored E4M3 number is that
+    of the IEEE fp32 quotient, clamped."""
+    kv, page = 8, 64
+    every = torch.arange(65536, dtype=torch.int32).to(torch.uint16).view(torch.bfloat16).view(64, kv, 128)
+    every = every.repeat(kv, 1, 1)  # each number under each head's scale
+    for h in range(kv):
+        every[64 * h:64 * h + 64] = every[64 * h:64 * h + 64].roll(h, 1)
+    g = torch.Generator().manual_seed(low)
+    for _ in range(4):
+        scale = (torch.rand(kv, generator=g) + 1) * 2.0 ** torch.randint(low, high, (kv,), generator=g)
+        kc, vc = (torch.zeros(8, kv, page, 128).to(torch.float8_e4m3fn).cuda() for _ in range(2))
+        dev, ds = every.cuda(), scale.cuda()
+        api.page_write(dev, dev, ints(list(range(512))), kc, vc, ds, ds)
+        ok(api)
+        want = (every.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+        got = kc.cpu().transpose(1, 2).reshape(512, kv, 128)
+        same = (got.view(torch.uint8) == want.view(torch.uint8)) | (got.float().isnan() & want.float().isnan())
+        assert same.all(), (every[~same][:5], scale)
+
+
 def test_write_reports_bad_slots(api):
     kc, vc = (torch.zeros(3, 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     k = torch.ones(5, 2, 128, dtype=torch.bfloat16, device="cuda")
