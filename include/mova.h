@@ -548,7 +548,10 @@ mova_status mova_page_bounds(const mova_pages* pages, const int32_t* table, long
  * pages (numbers j within the request's row) count, for each KV head its own.
  * Of each list the first min(top, pages of the request) entries are read;
  * one that is no page of the request (-1) is skipped; one given twice counts
- * twice.  Lengths are clamped to [0, max_pages * page_size] and reported. */
+ * twice.  Lengths are clamped to [0, max_pages * page_size] and reported.
+ * NaN and infinite keys or values that count show in o as the formula has it,
+ * except that with fp32 pages and more than 4 query heads to a KV head an
+ * infinite one shows as NaN. */
 mova_status mova_page_attend(const void* q, mova_dtype q_dt, long long q_stride, int H, const mova_pages* pages,
                              const int32_t* table, long long table_stride, int max_pages, const int32_t* lens, int B,
                              float scale, const int32_t* picked, int top, void* o, float* lse, void* ws,

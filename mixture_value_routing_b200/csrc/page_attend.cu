@@ -34,8 +34,18 @@
 // as the output's own rounding.  E4M3: K, V become fp16 exactly; q is scaled
 // by a power of two to [1, 2) at its largest element and rounded to fp16
 // (exact for elements down to 2^-14 of the largest); P in fp16 (2^-11 against
-// the output's 2^-8).  fp32: plain FMAs, whose rate is enough for 8 bytes per
-// token, head and dimension.
+// the output's 2^-8).  fp32, up to 4 query heads a KV head: plain FMAs, whose
+// rate is enough for 8 bytes per token, head and dimension.  fp32, more heads:
+// the FMAs and their operands from shared memory would bound it (16 heads: 470
+// us for 1.1 GB), so every fp32 number is split exactly into three bf16 parts
+// and six products of parts are formed by mma (225 us); there an infinite key
+// or value shows as NaN.
+//
+// Measured, of 6459 GB/s: bf16 16 requests to 32768 tokens, 775 MB: 124 us,
+// 97%; 64 x 4096 tokens, 1.1 GB: 168.6 us, 99% with 4 heads, 92% with 16; E4M3
+// 64 requests to 8192, 463 MB: 82 us, 88%; fp32 32 x 4096: 168 us, 99% with 4
+// heads, 73% with 7.  8 requests to 500 tokens: 7.8 us, the latency of two
+// launches and four dependent loads.
 #include <math.h>
 
 #include <algorithm>
@@ -51,20 +61,19 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStageBytes = 8192;  // K and V of one warp's tile
 constexpr int kRingAlign = 256;
-#ifndef ST_F32
-#define ST_F32 2
-#define ST_B16 3
-#define ST_E8 2
-#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-enum Mode { kF32 = 0, kB16 = 1, kE8 = 2 };
+// fp32 pages by FMAs (up to 4 query heads a KV head) or by matrix products of
+// bf16 parts; bf16 pages; E4M3 pages.
+enum Mode { kF32 = 0, kB16 = 1, kE8 = 2, kF32Parts = 3 };
+template <int M> constexpr bool kIsF32 = M == kF32 || M == kF32Parts;
 
 template <int M> struct Tile;  // of one warp
-template <> struct Tile<kF32> { using E = float;         static constexpr int keys = 8;  static constexpr int groups = 1; static constexpr int stages = ST_F32; };
-template <> struct Tile<kB16> { using E = __nv_bfloat16; static constexpr int keys = 16; static constexpr int groups = 1; static constexpr int stages = ST_B16; };
-template <> struct Tile<kE8>  { using E = uint8_t;       static constexpr int keys = 32; static constexpr int groups = 2; static constexpr int stages = ST_E8; };
+template <> struct Tile<kF32> { using E = float;         static constexpr int keys = 8;  static constexpr int groups = 1; static constexpr int stages = 2; };
+template <> struct Tile<kF32Parts> : Tile<kF32> {};
+template <> struct Tile<kB16> { using E = __nv_bfloat16; static constexpr int keys = 16; static constexpr int groups = 1; static constexpr int stages = 3; };
+template <> struct Tile<kE8>  { using E = uint8_t;       static constexpr int keys = 32; static constexpr int groups = 2; static constexpr int stages = 2; };
 
 struct AttendArgs {
   PageArgs a;
@@ -151,8 +160,8 @@ __device__ __forceinline__ float ex2(float x) {
 // The maximum to subtract: 0 while nothing has been seen.
 __device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.0f : m; }
 
-// One warp's softmax state for up to NT x 8 heads (mma) or NT heads (fp32).
-// mma: column heads nt * 8 + 2 * (lane & 3) + {0, 1}; fp32: all heads.
+// One warp's softmax state for up to NT x 8 heads (mma) or NT heads (FMAs).
+// mma: column heads nt * 8 + 2 * (lane & 3) + {0, 1}; FMAs: all heads.
 template <int M, int NT> struct State {
   float o[M == kF32 ? 1 : 8][NT][4];
   float m[NT][2], l[NT][2];
@@ -370,9 +379,14 @@ __device__ __forceinline__ void tile_e8(State<kE8, NT>& st, const Query<kE8, NT>
   }
 }
 
-// One tile of 8 fp32 keys: rows of 512 bytes, chunk c of row r at
-// c ^ ((r & 1) << 2).  Scores: four lanes per key, 32 dimensions each; then
-// each lane holds dimensions 4 * lane + {0..3} of the output.  NT heads.
+// fp32 rows are 512 bytes, chunk c of row r at place c ^ f32_swizzle(r): four
+// chunks of two neighbouring rows, and two of every second row, then lie in
+// different banks.
+__host__ __device__ constexpr int f32_swizzle(int r) { return ((r >> 1 & 3) << 1) ^ ((r & 1) << 2); }
+
+// One tile of 8 fp32 keys, by FMAs.  Scores: four lanes per key, 32 dimensions
+// each; then each lane holds dimensions 4 * lane + {0..3} of the output.  NT
+// heads.
 template <int NT>
 __device__ __forceinline__ void tile_f32(State<kF32, NT>& st, const float* q, float scale, const char* kt,
                                          const char* vt, int valid, int lane) {
@@ -383,7 +397,7 @@ __device__ __forceinline__ void tile_f32(State<kF32, NT>& st, const float* q, fl
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int c = part + 4 * i;
-    const float4 k = *reinterpret_cast<const float4*>(kt + key * 512 + ((c ^ ((key & 1) << 2)) << 4));
+    const float4 k = *reinterpret_cast<const float4*>(kt + key * 512 + ((c ^ f32_swizzle(key)) << 4));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float4 x = *reinterpret_cast<const float4*>(q + n * kHeadDim + 4 * c);
@@ -408,7 +422,7 @@ __device__ __forceinline__ void tile_f32(State<kF32, NT>& st, const float* q, fl
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float4 v = *reinterpret_cast<const float4*>(vt + j * 512 + ((lane ^ ((j & 1) << 2)) << 4));
+    const float4 v = *reinterpret_cast<const float4*>(vt + j * 512 + ((lane ^ f32_swizzle(j)) << 4));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const float p = __shfl_sync(0xffffffffu, s[n], 4 * j);
@@ -416,6 +430,123 @@ __device__ __forceinline__ void tile_f32(State<kF32, NT>& st, const float* q, fl
       st.o[0][n][1] = fmaf(p, v.y, st.o[0][n][1]);
       st.o[0][n][2] = fmaf(p, v.z, st.o[0][n][2]);
       st.o[0][n][3] = fmaf(p, v.w, st.o[0][n][3]);
+    }
+  }
+}
+
+// Three bf16 numbers whose sum is x exactly (8 + 8 + 8 significand bits, each
+// truncated), as the upper halves of fp32 words.
+__device__ __forceinline__ void split3(float x, uint32_t (&p)[3]) {
+  p[0] = __float_as_uint(x) & 0xffff0000u;
+  const float r = x - __uint_as_float(p[0]);
+  p[1] = __float_as_uint(r) & 0xffff0000u;
+  p[2] = __float_as_uint(r - __uint_as_float(p[1]));
+}
+// The parts of two numbers, packed.
+__device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3]) {
+  uint32_t a[3], b[3];
+  split3(x, a);
+  split3(y, b);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) p[i] = __byte_perm(a[i], b[i], 0x7632);
+}
+
+// fp32 by parts: heads g and g + 8 (NT = 2) of the rows of S = q K^T and
+// O = P V.  Output tile 4 c + j holds dimensions 32 c + 4 n + j in column n, so
+// a lane's columns 2 t and 2 t + 1 of tiles 4 c .. 4 c + 3 are dimensions
+// 32 c + 8 t .. + 7.
+template <int NT> struct State<kF32Parts, NT> {
+  float o[16][4];
+  float m[2], l[2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[i][c] = 0.0f;
+    m[0] = m[1] = -INFINITY, l[0] = l[1] = 0.0f;
+  }
+};
+template <int NT> struct Query<kF32Parts, NT> {
+  uint32_t a[3][8][2 * NT];  // parts; steps of 16 dimensions; row operand words of heads g (and g + 8)
+};
+template <int NT>
+__device__ __forceinline__ void load_query_parts(Query<kF32Parts, NT>& r, const float* q, int G, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int head = n * 8 + g;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float4 x = head < G ? *reinterpret_cast<const float4*>(q + head * kHeadDim + 16 * k + 4 * t)
+                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      uint32_t p[3], s[3];
+      split3(x.x, x.y, p);
+      split3(x.z, x.w, s);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) r.a[i][k][n] = p[i], r.a[i][k][NT + n] = s[i];
+    }
+  }
+}
+
+// One tile of 8 fp32 keys by matrix products: with every fp32 number the sum of
+// three bf16 parts, a product keeps the six pairs of parts down to 2^-16 of it
+// (what is left out is below 2^-23).  A lane's four loaded dimensions 4 t ..
+// 4 t + 3 of a step of 16 are the step's k = 2t, 2t + 1, 2t + 8, 2t + 9.
+template <int NT>
+__device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Query<kF32Parts, NT>& q, float scale,
+                                               const char* kt, const char* vt, int valid, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float4 x = *reinterpret_cast<const float4*>(kt + g * 512 + (((4 * k + t) ^ f32_swizzle(g)) << 4));
+    uint32_t lo[3], hi[3];
+    split3(x.x, x.y, lo);
+    split3(x.z, x.w, hi);
+    // The small pairs first, apart from the large one.
+#pragma unroll
+    for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+      for (int i = 0; i <= sum; ++i)
+        mma16816<kB16>(s[sum == 0 ? 0 : 1], q.a[i][k][0], NT > 1 ? q.a[i][k][NT - 1] : 0u, q.a[i][k][NT],
+                       NT > 1 ? q.a[i][k][2 * NT - 1] : 0u, lo[sum - i], hi[sum - i]);
+  }
+  uint32_t p[2][3];  // parts of P: heads g and g + 8, keys 2t, 2t + 1
+#pragma unroll
+  for (int r = 0; r < NT; ++r) {
+    float x[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) x[c] = 2 * t + c < valid ? (s[0][2 * r + c] + s[1][2 * r + c]) * scale : -INFINITY;
+    float top = fmaxf(x[0], x[1]);
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const float m = fmaxf(st.m[r], top);
+    if (__any_sync(0xffffffffu, m > st.m[r])) {
+      const float a = ex2(st.m[r] - ref_of(m));
+      st.l[r] *= a;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st.o[i][2 * r] *= a, st.o[i][2 * r + 1] *= a;
+    }
+    st.m[r] = m;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) x[c] = ex2(x[c] - ref_of(m));
+    st.l[r] += x[0] + x[1];
+    split3(x[0], x[1], p[r]);
+  }
+  if (NT == 1) p[1][0] = p[1][1] = p[1][2] = 0u;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float4 x = *reinterpret_cast<const float4*>(vt + 2 * t * 512 + (((8 * c + g) ^ f32_swizzle(2 * t)) << 4));
+    const float4 y = *reinterpret_cast<const float4*>(vt + (2 * t + 1) * 512 + (((8 * c + g) ^ f32_swizzle(2 * t + 1)) << 4));
+    const float xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t v[3];
+      split3(xs[j], ys[j], v);
+      // Two pairs of parts at a time, one in each half of the 16 keys' places.
+      mma16816<kB16>(st.o[4 * c + j], p[0][0], p[1][0], p[0][1], p[1][1], v[2], v[1]);
+      mma16816<kB16>(st.o[4 * c + j], p[0][2], p[1][2], p[0][0], p[1][0], v[0], v[1]);
+      mma16816<kB16>(st.o[4 * c + j], p[0][1], p[1][1], p[0][0], p[1][0], v[0], v[0]);
     }
   }
 }
@@ -452,7 +583,7 @@ __device__ __forceinline__ int turn_swizzle(int head) { return ((head >> 1) & 3)
 
 // Four consecutive outputs of one head.
 template <int M> __device__ __forceinline__ void store_out(void* o, long long at, const float4& v) {
-  if constexpr (M == kF32)
+  if constexpr (kIsF32<M>)
     *reinterpret_cast<float4*>(static_cast<float*>(o) + at) = v;
   else
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
@@ -462,7 +593,7 @@ template <int M> __device__ __forceinline__ void store_out(void* o, long long at
 template <int M, int NT, int kTeam>
 __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs s) {
   using E = typename Tile<M>::E;
-  using Out = typename std::conditional<M == kF32, float, __nv_bfloat16>::type;
+  using Out = typename std::conditional<kIsF32<M>, float, __nv_bfloat16>::type;
   constexpr int kKeys = Tile<M>::keys;
   constexpr int kUnit = kTeam * kKeys;
   constexpr int kGroups = Tile<M>::groups;
@@ -546,13 +677,13 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
   const char* v_base = static_cast<const char*>(s.a.v);
   constexpr int kRowsPer = 32 / kChunks;               // rows of one warp-wide copy
   constexpr int kCopies = kKeys / kGroups / kRowsPer;  // of K, and of V, per group
-  constexpr int kPeriod = M == kF32 ? 2 : 8 / kRowsPer;  // copies after which the swizzle repeats
+  constexpr int kPeriod = 8 / kRowsPer;  // copies after which the swizzle repeats
   const int lane_off = (lane / kChunks) * kRow + (lane % kChunks) * 16;
   uint32_t swz[kPeriod];
 #pragma unroll
   for (int x = 0; x < kPeriod; ++x) {
     const int r = x * kRowsPer + lane / kChunks, c = lane % kChunks;
-    swz[x] = r * kRow + ((M == kF32 ? c ^ ((r & 1) << 2) : c ^ (r & 7)) << 4);
+    swz[x] = r * kRow + ((kIsF32<M> ? c ^ f32_swizzle(r) : c ^ (r & 7)) << 4);
   }
   // Starts the copies of tile i (of this warp) into its stage.  Where a new row
   // begins, its queries are called into the cache: they are needed with its keys.
@@ -564,8 +695,8 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
       if (owner != ahead) {
         ahead = owner;
         const int line = lane * 128;
-        if (line < G * kHeadDim * (M == kF32 ? 4 : 2)) {
-          const char* at = static_cast<const char*>(s.q) + q_at(owner) * (M == kF32 ? 4 : 2) + line;
+        if (line < G * kHeadDim * (kIsF32<M> ? 4 : 2)) {
+          const char* at = static_cast<const char*>(s.q) + q_at(owner) * (kIsF32<M> ? 4 : 2) + line;
           asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
         }
       }
@@ -622,6 +753,8 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
             reinterpret_cast<float4*>(q_sm)[x] =
                 4 * x < G * kHeadDim ? reinterpret_cast<const float4*>(src)[x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           if constexpr (kTeam > 1) __syncthreads();
+        } else if constexpr (M == kF32Parts) {
+          load_query_parts<NT>(q, static_cast<const float*>(s.q) + at, G, lane);
         } else {
           const float k_scale = M == kE8 && s.a.k_scale != nullptr ? s.a.k_scale[h] : 1.0f;
           load_query<M, NT>(q, static_cast<const __nv_bfloat16*>(s.q) + at, G, s.scale * kLog2e * k_scale, lane);
@@ -638,6 +771,8 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
         tile_b16<NT>(st, q, kt, vt, sm_valid[warp][stage][0], lane);
       } else if constexpr (M == kE8) {
         tile_e8<NT>(st, q, kt, vt, sm_valid[warp][stage][0], sm_valid[warp][stage][1], lane);
+      } else if constexpr (M == kF32Parts) {
+        tile_f32_parts<NT>(st, q, s.scale * kLog2e, tile, tile + kStageBytes / 2, sm_valid[warp][stage][0], lane);
       } else {
         tile_f32<NT>(st, q_sm, s.scale * kLog2e, tile, tile + kStageBytes / 2, sm_valid[warp][stage][0], lane);
       }
@@ -669,6 +804,12 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
             *reinterpret_cast<float4*>(part + head * kHeadDim + 4 * lane) = v;
           if (lane == 0) note(head, m, l);
         };
+        auto put_all = [&] {
+          __syncwarp();
+          for (int head = 0; head < G; ++head)
+            put(head, sm_m[warp][head], sm_l[warp][head],
+                *reinterpret_cast<const float4*>(&turn[head * kHeadDim + ((4 * lane) ^ turn_swizzle(head))]));
+        };
         __syncwarp();  // every lane has read the tile
         if constexpr (M == kF32) {
 #pragma unroll
@@ -686,6 +827,28 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
               }
             }
           }
+        } else if constexpr (M == kF32Parts) {
+          const int g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float l = st.l[n];
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            const int head = n * 8 + g;
+            if (head < G) {
+              if (t4 == 0) sm_m[warp][head] = st.m[n], sm_l[warp][head] = l;
+              float* to = &turn[head * kHeadDim];
+              const int z = turn_swizzle(head);
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  *reinterpret_cast<float4*>(&to[(32 * c + 8 * t4 + 4 * x) ^ z]) =
+                      make_float4(st.o[4 * c][2 * n + x], st.o[4 * c + 1][2 * n + x], st.o[4 * c + 2][2 * n + x],
+                                  st.o[4 * c + 3][2 * n + x]);
+            }
+          }
+          if constexpr (kTeam == 1) put_all();
         } else {
           const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll
@@ -711,12 +874,7 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
                 }
               }
             }
-          if constexpr (kTeam == 1) {
-            __syncwarp();
-            for (int head = 0; head < G; ++head)
-              put(head, sm_m[warp][head], sm_l[warp][head],
-                  *reinterpret_cast<const float4*>(&turn[head * kHeadDim + ((4 * lane) ^ turn_swizzle(head))]));
-          }
+          if constexpr (kTeam == 1) put_all();
         }
         if constexpr (kTeam == 1) {
           __syncwarp();  // q_sm, sm_m and sm_l are free again
@@ -915,8 +1073,8 @@ cudaError_t launch_page_attend(const void* q, long long q_stride, int G, const P
   const AttendArgs s{a, q, q_stride, G, scale, picked, top, o, lse, ws.bad, ws.prefix, ws.part};
   if (dt == MOVA_F32) {
     if (G <= 4) return launch_attend<kF32, 4>(s, ws.sb, stream);
-    if (G <= 8) return launch_attend<kF32, 8>(s, ws.sb, stream);
-    return launch_attend<kF32, 16>(s, ws.sb, stream);
+    if (G <= 8) return launch_attend<kF32Parts, 1>(s, ws.sb, stream);
+    return launch_attend<kF32Parts, 2>(s, ws.sb, stream);
   }
   if (dt == MOVA_BF16) {
     if (G <= 8) return launch_attend<kB16, 1>(s, ws.sb, stream);
