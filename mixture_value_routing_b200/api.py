@@ -50,6 +50,13 @@ except AttributeError:  # pragma: no cover - a torch built without CUDA
     _current_device = torch.cuda.current_device
 
 
+try:
+    _capturing = torch._C._cuda_isCurrentStreamCapturing
+except AttributeError:  # pragma: no cover - a torch built without CUDA
+    def _capturing() -> bool:
+        return False
+
+
 def _current_stream_handle() -> int:
     """The handle of the current stream of the current device."""
     if _raw_stream is not None:
@@ -581,9 +588,14 @@ def _table(index: int, table, B: int):
 
 def _page_ws(ws, nbytes: int, dev):
     """(address, bytes, stream handle): `ws`, or the current stream's workspace
-    on `dev`, the current device."""
+    on `dev`, the current device.  A call that a graph captures gets one of the
+    graph's own memory instead: graphs captured on one stream may be replayed on
+    several, and the stream's workspace may grow and move."""
     handle = _raw_stream(dev.index) if _raw_stream is not None else _current_stream_handle()
     if ws is None:
+        if _capturing():
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            return ws.data_ptr(), nbytes, handle
         own = _WS.get((dev, handle))
         ws = own.buf if own is not None else None
         if ws is None or ws.numel() < nbytes:

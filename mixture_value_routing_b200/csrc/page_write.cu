@@ -21,6 +21,16 @@ namespace mova {
 
 namespace {
 
+// A 16-byte load of data that is read once.  Not a read-only (.nc) load, and no
+// pointer here is __restrict__: the kernel before this one on the stream may
+// have written the data while this one was already launched.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p), "l"(evict_first_policy()) : "memory");
+  return r;
+}
+
 constexpr int kWriteSmall = 1024;  // CTAs of 512 threads from this many tokens on, 256 below
 
 // x / scale as IEEE division rounds it, from r, the rounded reciprocal of scale:
@@ -41,7 +51,7 @@ template <typename In, typename Out> struct Unit {
   uint4 x[kLoads];
   __device__ __forceinline__ void load(const In* p) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) x[i] = ld_stream_u4(p + i * (16 / sizeof(In)));
+    for (int i = 0; i < kLoads; ++i) x[i] = load_once(p + i * (16 / sizeof(In)));
   }
   __device__ __forceinline__ void store(Out* p, float scale) const {
     if constexpr (sizeof(Out) > 1)
@@ -78,8 +88,8 @@ template <typename In, typename Out> struct Unit {
 
 template <typename In, typename Out, int kThreads>
 __global__ void __launch_bounds__(kThreads)
-page_write_kernel(const In* __restrict__ k, const In* __restrict__ v, long long k_stride, long long v_stride,
-                  const int32_t* __restrict__ slots, int T, Out* __restrict__ kc, Out* __restrict__ vc,
+page_write_kernel(const In* k, const In* v, long long k_stride, long long v_stride,
+                  const int32_t* slots, int T, Out* kc, Out* vc,
                   long long kp_stride, long long vp_stride, const float* k_scale, const float* v_scale, int kv,
                   int shift, int num_slots, int lanes, StatusBlock* sb) {
   using U = Unit<In, Out>;
@@ -231,7 +241,7 @@ template <> struct Range<uint8_t> {
 
 template <typename E>
 __global__ void __launch_bounds__(kBoundThreads)
-page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __restrict__ lo, E* __restrict__ hi,
+page_bounds_kernel(const PageArgs a, const int32_t* cached, E* lo, E* hi,
                    StatusBlock* sb) {
   using R = Range<E>;
   constexpr int kPer = 16 / sizeof(E);
@@ -315,7 +325,7 @@ page_bounds_kernel(const PageArgs a, const int32_t* __restrict__ cached, E* __re
       for (int r = 0; r < rows; r += 16) {
         uint4 raw[kLoads];
 #pragma unroll
-        for (int y = 0; y < kLoads; ++y) raw[y] = ld_stream_u4(src + (r + y * kRows) * kHeadDim);
+        for (int y = 0; y < kLoads; ++y) raw[y] = load_once(src + (r + y * kRows) * kHeadDim);
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
           uint32_t v[R::kWords];

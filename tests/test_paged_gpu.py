@@ -268,7 +268,7 @@ def test_attend_edges(api, dtype, kv, G, page):
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
 @pytest.mark.parametrize("lens,kv,G,page", [
     ([1], 8, 4, 64), ([7, 0, 0], 8, 4, 16), ([20011], 2, 4, 64), ([9000, 1, 3500, 0, 12], 4, 5, 32), ([2049] * 3, 8, 1, 128),
-    ([30] * 600, 2, 3, 16),
+    ([30] * 600, 2, 3, 16), ([5] * 300 + [3000, 0, 700], 4, 9, 32), ([17] * 1100 + [2500], 1, 6, 16), ([1] * 1030, 1, 1, 256),
 ])
 def test_attend_lengths(api, dtype, lens, kv, G, page):
     check_attend(api, P.make(dtype, lens, kv, G, page, seed=len(lens)), dtype)
@@ -575,6 +575,39 @@ def test_captured_step_follows_its_inputs(api):
     assert a["cached"].tolist() == [40, 55, 56, 140, 0]
     wo, _, to, _ = P.attend(q, a["kc"], a["vc"], a["table"], a["cached"], dtype="bf16")
     assert ((P.f64(captured[3]) - wo).abs() <= to).all()
+
+
+def test_captured_calls_have_their_own_workspaces(api):
+    """Two graphs captured on one stream, replayed at once on two, and again after
+    the stream's own workspace has been replaced by a larger one."""
+    states = [P.make("bf16", [3000 + 500 * x, 1, 300], 8, 4, 64, seed=x) for x in range(2)]
+    alone = [api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"]) for s in states]
+    side = torch.cuda.Stream()
+    graphs, outs = [], []
+    for s in states:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            outs.append(api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"]))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in states]
+    for _ in range(30):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, want in zip(outs, alone):
+        assert torch.equal(o, want)
+    big = P.make("bf16", [40] * 64, 8, 16, 16, seed=5)
+    with torch.cuda.stream(side):
+        api.page_attend(big["q"], big["k"], big["v"], big["table"], big["lens"])
+        filler = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for o, want in zip(outs, alone):
+        assert torch.equal(o, want)
+    assert (filler == 255).all()
 
 
 # ---- With the value path ----------------------------------------------------------------
