@@ -557,17 +557,12 @@ __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Q
 // latency repays.
 template <int M, int kTeam> constexpr int kLeast = kTeam > 1 ? 1 : Tile<M>::stages;
 
-// The workers that take part, U units in all; the first unit of worker w of W
-// <= U, and the worker of unit u.  Every worker has a unit, so every one
-// between a row's first and last leaves a partial result.
-template <int M, int kTeam> __device__ __forceinline__ int workers_for(int ctas, int U) {
-  return min(ctas * (kWarps / kTeam), (U + kLeast<M, kTeam> - 1) / kLeast<M, kTeam>);
-}
-__device__ __forceinline__ int first_unit(int w, int W, int U) {
-  return static_cast<int>(static_cast<long long>(w) * U / W);
-}
-__device__ __forceinline__ int worker_of(int u, int W, int U) {
-  return static_cast<int>((static_cast<long long>(u + 1) * W - 1) / U);
+// Units of each worker, U in all (the last worker may have fewer): worker w
+// begins at unit w * share.  Whole shares, so that rows of one length are cut
+// alike, and often at their ends.
+template <int M, int kTeam> __device__ __forceinline__ int share_of(int ctas, int U) {
+  const int workers = ctas * (kWarps / kTeam);
+  return max(kLeast<M, kTeam>, (U + workers - 1) / workers);
 }
 
 // Dynamic shared memory: the rings, each worker's fp32 queries (NT heads), the prefix.
@@ -625,8 +620,8 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
   const int U = kv * pre[B];
   if (blockIdx.x == 0)
     for (int b = tid; b <= B; b += kThreads) s.prefix[b] = pre[b];
-  const int w = (blockIdx.x * kWarps + warp) / kTeam, W = workers_for<M, kTeam>(gridDim.x, U);
-  const int u0 = w < W ? first_unit(w, W, U) : 0, count = w < W ? first_unit(w + 1, W, U) - u0 : 0;
+  const int w = (blockIdx.x * kWarps + warp) / kTeam, share = share_of<M, kTeam>(gridDim.x, U);
+  const int u0 = min(w * share, U), count = min(share, U - u0);
 
   // Page lookup of 32 tiles: lane i that of this warp's tile in unit `at + i`,
   // with the row (request, KV head) that it belongs to.
@@ -961,9 +956,8 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
     if (group == 0) write(make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY);
     return;
   }
-  const int W = workers_for<M, kTeam>(ctas, U);
-  const int u0 = kv * p0 + h * tiles;
-  const int w0 = worker_of(u0, W, U), parts = worker_of(u0 + tiles - 1, W, U) - w0 + 1;
+  const int share = share_of<M, kTeam>(ctas, U), u0 = kv * p0 + h * tiles;
+  const int w0 = u0 / share, parts = (u0 + tiles - 1) / share - w0 + 1;
   if (parts == 1) return;
   const int size = G * kPartRow;
   // Worker w0 begins this row (its second place), the others continue it.
