@@ -557,19 +557,38 @@ __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Q
 // latency repays.
 template <int M, int kTeam> constexpr int kLeast = kTeam > 1 ? 1 : Tile<M>::stages;
 
-// Units of each worker, U in all (the last worker may have fewer): worker w
-// begins at unit w * share.  Whole shares, so that rows of one length are cut
-// alike, and often at their ends.
-template <int M, int kTeam> __device__ __forceinline__ int share_of(int ctas, int U) {
-  const int workers = ctas * (kWarps / kTeam);
-  return max(kLeast<M, kTeam>, (U + workers - 1) / workers);
-}
+// How U units are shared out: worker w takes units first(w) up to first(w + 1).
+// Small shares are whole numbers of units, so that rows of one length are cut
+// alike, and often at their ends (8 requests of 500 tokens: 8.4 us, 10.3 in
+// equal fractions); large ones equal fractions (64 ragged requests to 8192
+// tokens, E4M3: 82 us, 88 in whole numbers).  Either way every worker before
+// the last that has a unit has one, so that every one between a row's first and
+// last leaves a partial result.
+template <int M, int kTeam> struct Shares {
+  int U, W, share;  // share: 0 for fractions
+  __device__ __forceinline__ Shares(int ctas, int units) : U(units), W(ctas * (kWarps / kTeam)) {
+    share = max(kLeast<M, kTeam>, (U + W - 1) / W);
+    if (share > 8) share = 0;
+  }
+  __device__ __forceinline__ int first(int w) const {
+    return share > 0 ? min(w * share, U) : static_cast<int>(static_cast<long long>(w) * U / W);  // w, share: small
+  }
+  __device__ __forceinline__ int owner(int u) const {
+    return share > 0 ? u / share : static_cast<int>((static_cast<long long>(u + 1) * W - 1) / U);
+  }
+};
 
 // Dynamic shared memory: the rings, each worker's fp32 queries (NT heads), the prefix.
 template <int M, int NT, int kTeam>
 __host__ __device__ constexpr size_t attend_smem(int B) {
   return kRingAlign + kWarps * Tile<M>::stages * kStageBytes +
          (M == kF32 ? kWarps / kTeam * NT * kHeadDim * 4 : 0) + static_cast<size_t>(B + 1) * 4;
+}
+
+// CTAs of an SM, by registers: as many as shared memory allows for the stages, or
+// two where the state of 16 heads or of fp32 parts needs the registers.
+template <int M, int NT> __host__ __device__ constexpr int ctas_per_sm() {
+  return M == kF32 || (M == kE8 && NT == 1) ? 3 : 2;
 }
 
 // Where a warp turns its outputs round, head's dimension d lies at
@@ -586,7 +605,7 @@ template <int M> __device__ __forceinline__ void store_out(void* o, long long at
 
 // NT: mma column tiles of 8 heads, or fp32 heads.
 template <int M, int NT, int kTeam>
-__global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs s) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_kernel(const AttendArgs s) {
   using E = typename Tile<M>::E;
   using Out = typename std::conditional<kIsF32<M>, float, __nv_bfloat16>::type;
   constexpr int kKeys = Tile<M>::keys;
@@ -620,8 +639,8 @@ __global__ void __launch_bounds__(kThreads) page_attend_kernel(const AttendArgs 
   const int U = kv * pre[B];
   if (blockIdx.x == 0)
     for (int b = tid; b <= B; b += kThreads) s.prefix[b] = pre[b];
-  const int w = (blockIdx.x * kWarps + warp) / kTeam, share = share_of<M, kTeam>(gridDim.x, U);
-  const int u0 = min(w * share, U), count = min(share, U - u0);
+  const Shares<M, kTeam> shares(gridDim.x, U);
+  const int w = (blockIdx.x * kWarps + warp) / kTeam, u0 = shares.first(w), count = shares.first(w + 1) - u0;
 
   // Page lookup of 32 tiles: lane i that of this warp's tile in unit `at + i`,
   // with the row (request, KV head) that it belongs to.
@@ -956,8 +975,8 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
     if (group == 0) write(make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY);
     return;
   }
-  const int share = share_of<M, kTeam>(ctas, U), u0 = kv * p0 + h * tiles;
-  const int w0 = u0 / share, parts = (u0 + tiles - 1) / share - w0 + 1;
+  const Shares<M, kTeam> shares(ctas, U);
+  const int u0 = kv * p0 + h * tiles, w0 = shares.owner(u0), parts = shares.owner(u0 + tiles - 1) - w0 + 1;
   if (parts == 1) return;
   const int size = G * kPartRow;
   // Worker w0 begins this row (its second place), the others continue it.
@@ -1017,15 +1036,8 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   cudaError_t err = prepare_kernel(kern, attend_smem<M, NT, kTeam>(kMaxRequests), done);
   if (err != cudaSuccess) return err;
   const size_t smem = attend_smem<M, NT, kTeam>(s.a.B);
-  // CTAs an SM holds at once, by shared memory and registers; all are resident,
-  // as each takes an equal share.  More than three gain nothing.
-  static const int regs = [] {
-    cudaFuncAttributes at{};
-    return cudaFuncGetAttributes(&at, page_attend_kernel<M, NT, kTeam>) == cudaSuccess && at.numRegs > 0 ? at.numRegs
-                                                                                                      : 255;
-  }();
-  const int by_regs = 65536 / (((regs + 7) & ~7) * kThreads);
-  const int per_sm = std::max(1, std::min({3, by_regs, static_cast<int>((227 * 1024) / (smem + 2048))}));
+  // All CTAs are resident at once, as each takes an equal share.
+  const int per_sm = std::max(1, std::min(ctas_per_sm<M, NT>(), static_cast<int>((227 * 1024) / (smem + 2048))));
   constexpr int kCta = kWarps * kLeast<M, kTeam> * Tile<M>::keys;  // tokens that keep a CTA busy
   const long long tokens = s.picked == nullptr ? static_cast<long long>(s.a.max_pages) << s.a.shift
                                                : static_cast<long long>(std::min(s.top, s.a.max_pages)) << s.a.shift;

@@ -34,7 +34,6 @@ constexpr int kScoreWarps = kScoreThreads / 32;
 // CTAs of the score kernel an SM: by the registers of its NT tiles of heads.
 constexpr int score_per_sm(int NT) { return NT == 1 ? 3 : 2; }
 constexpr int kPages = 8;  // of one batch
-constexpr int kTopThreads = 512;
 constexpr int kDigit = 8;
 constexpr int kBins = 1 << kDigit;
 
@@ -317,7 +316,6 @@ __device__ __forceinline__ u64 warp_min(u64 x) {
 }
 
 constexpr int kHeld = 16;  // keys of a thread in registers; a long request's others are read again
-constexpr int kTopWarps = kTopThreads / 32;
 
 // Radix search among 32-bit values for the `need` greatest: each(f) calls f for
 // every value of this thread, whose upper `bits` are searched.  Returns how
@@ -373,7 +371,9 @@ __device__ __forceinline__ int radix_search(Each each, int bits, int (*hist)[kBi
   return bits;
 }
 
+template <int kTopThreads>
 __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs s, int score_ctas, StatusBlock* sb) {
+  constexpr int kTopWarps = kTopThreads / 32;
   constexpr int kDigits = 32 / kDigit;
   __shared__ int hist[2 * kDigits][kBins];
   __shared__ u64 sm_min[kTopWarps], sm_max[kTopWarps];
@@ -409,6 +409,22 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
   u64 held[kHeld], least = ~0ULL, most_inv = ~0ULL;  // the greatest, as the least complement
 #pragma unroll
   for (int i = 0; i < kHeld; ++i) held[i] = i < span && first + 32 * i < N ? keys[first + 32 * i] : 0ULL;
+  // Calls f(key, i) for every key i of this thread that is not held; loads eight
+  // at a time.
+  auto others = [&](auto f) {
+    constexpr int kAhead = 8;
+    for (int i0 = kHeld; i0 < span; i0 += kAhead) {
+      u64 k[kAhead];
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        const int at = first + 32 * (i0 + x);
+        k[x] = i0 + x < span && at < N ? keys[at] : 0ULL;
+      }
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        if (i0 + x < span) f(k[x], i0 + x);
+    }
+  };
   auto see = [&](u64 k) {
     least = k < least ? k : least;
     most_inv = ~k < most_inv ? ~k : most_inv;
@@ -418,8 +434,9 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     if (i >= span) break;
     if (first + 32 * i < N) see(held[i]);
   }
-  for (int i = kHeld; i < span; ++i)
-    if (first + 32 * i < N) see(keys[first + 32 * i]);
+  others([&](u64 k, int i) {
+    if (first + 32 * i < N) see(k);
+  });
   least = warp_min(least);
   most_inv = warp_min(most_inv);
   if (lane == 0) sm_min[warp] = least, sm_max[warp] = most_inv;
@@ -447,8 +464,9 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
           if (i >= span) break;
           if (first + 32 * i < N) f(v[i]);
         }
-        for (int i = kHeld; i < span; ++i)
-          if (first + 32 * i < N) f(upper(keys[first + 32 * i]));
+        others([&](u64 k, int i) {
+          if (first + 32 * i < N) f(upper(k));
+        });
       },
       open == 0 ? 0 : 32, hist, &p1, &need, &all);
   const bool second = open > 32 && !all;
@@ -471,7 +489,6 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     if (second && x == p) x = (static_cast<uint32_t>(keys[first + 32 * i]) & rest) >> r2, p = p2;
     return x > p ? 1 : x == p ? 2 : 0;
   };
-  auto value_of = [&](int i) { return upper(keys[first + 32 * i]); };
   // The warps' counts, one barrier, and out, in page order.
   int2 mine = make_int2(0, 0);
   auto count = [&](int at) {
@@ -483,7 +500,7 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     if (i >= span) break;
     count(place(i, v[i]));
   }
-  for (int i = kHeld; i < span; ++i) count(place(i, first + 32 * i < N ? value_of(i) : 0u));
+  others([&](u64 k, int i) { count(place(i, upper(k))); });
   if (lane == 0) sm_count[warp] = mine;
   __syncthreads();
   int more = 0, same = 0;
@@ -501,7 +518,7 @@ __global__ void __launch_bounds__(kTopThreads) page_top_kernel(const SelectArgs 
     if (i >= span) break;
     write(i, place(i, v[i]));
   }
-  for (int i = kHeld; i < span; ++i) write(i, place(i, first + 32 * i < N ? value_of(i) : 0u));
+  others([&](u64 k, int i) { write(i, place(i, upper(k))); });
 }
 
 template <typename Q, typename E, int NT>
@@ -515,6 +532,14 @@ cudaError_t launch_score_t(const SelectArgs& s, int ctas, cudaStream_t stream) {
 template <typename Q, typename E>
 cudaError_t launch_score(const SelectArgs& s, int ctas, cudaStream_t stream) {
   return s.G <= 8 ? launch_score_t<Q, E, 1>(s, ctas, stream) : launch_score_t<Q, E, 2>(s, ctas, stream);
+}
+
+template <int kTopThreads>
+cudaError_t launch_top(const SelectArgs& s, int score_ctas, StatusBlock* sb, cudaStream_t stream) {
+  static bool done[64] = {false};
+  const cudaError_t err = prepare_kernel(page_top_kernel<kTopThreads>, 0, done);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(page_top_kernel<kTopThreads>, dim3(s.a.B * s.a.kv), dim3(kTopThreads), 0, stream, s, score_ctas, sb);
 }
 
 }  // namespace
@@ -532,10 +557,9 @@ cudaError_t launch_page_select(const void* q, long long q_stride, int G, const P
   if (dt == MOVA_F32) err = launch_score<float, float>(s, n, stream);
   else if (dt == MOVA_BF16) err = launch_score<__nv_bfloat16, __nv_bfloat16>(s, n, stream);
   else err = launch_score<__nv_bfloat16, uint8_t>(s, n, stream);
-  static bool done[64] = {false};
-  if (err == cudaSuccess) err = prepare_kernel(page_top_kernel, 0, done);
   if (err != cudaSuccess) return err;
-  return launch_pdl(page_top_kernel, dim3(a.B * a.kv), dim3(kTopThreads), 0, stream, s, n, ws.sb);
+  // Twice the threads where a row may have more scores than 512 hold.
+  return a.max_pages > 512 * kHeld ? launch_top<1024>(s, n, ws.sb, stream) : launch_top<512>(s, n, ws.sb, stream);
 }
 
 }  // namespace mova

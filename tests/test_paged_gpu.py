@@ -420,7 +420,7 @@ def bounds_of(s, page):
 @pytest.mark.parametrize("lens,kv,G,page,top", [
     ([500], 2, 4, 16, 5), ([500, 16, 0, 17, 81, 1], 2, 4, 16, 1), ([500, 16, 0, 17, 81, 1], 3, 7, 16, 5),
     ([3000, 2999, 100, 1], 1, 16, 32, 40), ([12000, 700], 2, 1, 16, 64), ([900] * 40, 2, 2, 128, 3),
-    ([33000], 1, 8, 16, 1000),
+    ([33000], 1, 8, 16, 1000), ([140000, 300000], 1, 2, 16, 50),
 ])
 def test_select(api, dtype, lens, kv, G, page, top):
     s = P.make(dtype, lens, kv, G, page, seed=top)
