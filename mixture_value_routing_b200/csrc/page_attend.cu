@@ -557,26 +557,15 @@ __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Q
 // latency repays.
 template <int M, int kTeam> constexpr int kLeast = kTeam > 1 ? 1 : Tile<M>::stages;
 
-// How U units are shared out: worker w takes units first(w) up to first(w + 1).
-// Small shares are whole numbers of units, so that rows of one length are cut
-// alike, and often at their ends (8 requests of 500 tokens: 8.4 us, 10.3 in
-// equal fractions); large ones equal fractions (64 ragged requests to 8192
-// tokens, E4M3: 82 us, 88 in whole numbers).  Either way every worker before
-// the last that has a unit has one, so that every one between a row's first and
-// last leaves a partial result.
-template <int M, int kTeam> struct Shares {
-  int U, W, share;  // share: 0 for fractions
-  __device__ __forceinline__ Shares(int ctas, int units) : U(units), W(ctas * (kWarps / kTeam)) {
-    share = max(kLeast<M, kTeam>, (U + W - 1) / W);
-    if (share > 8) share = 0;
-  }
-  __device__ __forceinline__ int first(int w) const {
-    return share > 0 ? min(w * share, U) : static_cast<int>(static_cast<long long>(w) * U / W);  // w, share: small
-  }
-  __device__ __forceinline__ int owner(int u) const {
-    return share > 0 ? u / share : static_cast<int>((static_cast<long long>(u + 1) * W - 1) / U);
-  }
-};
+// Units of each worker, U in all (the last that has any may have fewer): worker
+// w begins at unit w * share, so every worker between a row's first and last
+// leaves a partial result.  Whole numbers of units, so that rows of one length
+// are cut alike, and often at their ends (8 requests of 500 tokens: 8.7 us, 10.3
+// in equal fractions of the units; long ones the same either way).
+template <int M, int kTeam> __device__ __forceinline__ int share_of(int ctas, int U) {
+  const int workers = ctas * (kWarps / kTeam);
+  return max(kLeast<M, kTeam>, (U + workers - 1) / workers);
+}
 
 // Dynamic shared memory: the rings, each worker's fp32 queries (NT heads), the prefix.
 template <int M, int NT, int kTeam>
@@ -639,8 +628,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
   const int U = kv * pre[B];
   if (blockIdx.x == 0)
     for (int b = tid; b <= B; b += kThreads) s.prefix[b] = pre[b];
-  const Shares<M, kTeam> shares(gridDim.x, U);
-  const int w = (blockIdx.x * kWarps + warp) / kTeam, u0 = shares.first(w), count = shares.first(w + 1) - u0;
+  const int w = (blockIdx.x * kWarps + warp) / kTeam, share = share_of<M, kTeam>(gridDim.x, U);
+  const int u0 = min(w * share, U), count = min(share, U - u0);
 
   // Page lookup of 32 tiles: lane i that of this warp's tile in unit `at + i`,
   // with the row (request, KV head) that it belongs to.
@@ -975,8 +964,8 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
     if (group == 0) write(make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY);
     return;
   }
-  const Shares<M, kTeam> shares(ctas, U);
-  const int u0 = kv * p0 + h * tiles, w0 = shares.owner(u0), parts = shares.owner(u0 + tiles - 1) - w0 + 1;
+  const int share = share_of<M, kTeam>(ctas, U), u0 = kv * p0 + h * tiles;
+  const int w0 = u0 / share, parts = (u0 + tiles - 1) / share - w0 + 1;
   if (parts == 1) return;
   const int size = G * kPartRow;
   // Worker w0 begins this row (its second place), the others continue it.
