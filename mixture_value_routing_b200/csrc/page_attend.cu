@@ -119,38 +119,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-template <int M>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  if constexpr (M == kB16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Two E4M3 values (low 16 bits of x, or high) as fp16, exactly.
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(x));
-  return r;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 p = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
 // 2^x for x <= 0 (or NaN), relative error 2^-22; below 2^-126 it is 0.
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -309,7 +281,7 @@ __device__ __forceinline__ void tile_b16(State<kB16, NT>& st, const Query<kB16, 
     uint32_t a[4];
     ldsm4(a, krow ^ (k << 5));
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mma16816<kB16>(s[k & 1][n], a[0], a[1], a[2], a[3], q.b[k][n][0], q.b[k][n][1]);
+    for (int n = 0; n < NT; ++n) mma16816<false>(s[k & 1][n], a[0], a[1], a[2], a[3], q.b[k][n][0], q.b[k][n][1]);
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n)
@@ -326,8 +298,8 @@ __device__ __forceinline__ void tile_b16(State<kB16, NT>& st, const Query<kB16, 
     ldsm4t(a, vrow ^ (i << 5));
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      mma16816<kB16>(st.o[i][n], a[0], a[1], a[2], a[3], p[0][n][0], p[0][n][1]);
-      mma16816<kB16>(st.o[i][n], a[0], a[1], a[2], a[3], plo[0][n][0], plo[0][n][1]);
+      mma16816<false>(st.o[i][n], a[0], a[1], a[2], a[3], p[0][n][0], p[0][n][1]);
+      mma16816<false>(st.o[i][n], a[0], a[1], a[2], a[3], plo[0][n][0], plo[0][n][1]);
     }
   }
 }
@@ -358,7 +330,7 @@ __device__ __forceinline__ void tile_e8(State<kE8, NT>& st, const Query<kE8, NT>
       const uint32_t a0 = e4m3_lo(a[2 * h]), a1 = e4m3_lo(a[2 * h + 1]);
       const uint32_t a2 = e4m3_hi(a[2 * h]), a3 = e4m3_hi(a[2 * h + 1]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma16816<kE8>(s[h][n], a0, a1, a2, a3, q.b[k][n][0], q.b[k][n][1]);
+      for (int n = 0; n < NT; ++n) mma16816<true>(s[h][n], a0, a1, a2, a3, q.b[k][n][0], q.b[k][n][1]);
     }
   }
   uint32_t p[2][NT][2], none[2][NT][2];
@@ -374,7 +346,7 @@ __device__ __forceinline__ void tile_e8(State<kE8, NT>& st, const Query<kE8, NT>
       const uint32_t x = __byte_perm(a[2 * h], 0, 0x3120), y = __byte_perm(a[2 * h + 1], 0, 0x3120);
       const uint32_t a0 = e4m3_lo(x), a1 = e4m3_hi(x), a2 = e4m3_lo(y), a3 = e4m3_hi(y);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma16816<kE8>(st.o[i][n], a0, a1, a2, a3, p[h][n][0], p[h][n][1]);
+      for (int n = 0; n < NT; ++n) mma16816<true>(st.o[i][n], a0, a1, a2, a3, p[h][n][0], p[h][n][1]);
     }
   }
 }
@@ -508,7 +480,7 @@ __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Q
     for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
       for (int i = 0; i <= sum; ++i)
-        mma16816<kB16>(s[sum == 0 ? 0 : 1], q.a[i][k][0], NT > 1 ? q.a[i][k][NT - 1] : 0u, q.a[i][k][NT],
+        mma16816<false>(s[sum == 0 ? 0 : 1], q.a[i][k][0], NT > 1 ? q.a[i][k][NT - 1] : 0u, q.a[i][k][NT],
                        NT > 1 ? q.a[i][k][2 * NT - 1] : 0u, lo[sum - i], hi[sum - i]);
   }
   uint32_t p[2][3];  // parts of P: heads g and g + 8, keys 2t, 2t + 1
@@ -544,9 +516,9 @@ __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Q
       uint32_t v[3];
       split3(xs[j], ys[j], v);
       // Two pairs of parts at a time, one in each half of the 16 keys' places.
-      mma16816<kB16>(st.o[4 * c + j], p[0][0], p[1][0], p[0][1], p[1][1], v[2], v[1]);
-      mma16816<kB16>(st.o[4 * c + j], p[0][2], p[1][2], p[0][0], p[1][0], v[0], v[1]);
-      mma16816<kB16>(st.o[4 * c + j], p[0][1], p[1][1], p[0][0], p[1][0], v[0], v[0]);
+      mma16816<false>(st.o[4 * c + j], p[0][0], p[1][0], p[0][1], p[1][1], v[2], v[1]);
+      mma16816<false>(st.o[4 * c + j], p[0][2], p[1][2], p[0][0], p[1][0], v[0], v[1]);
+      mma16816<false>(st.o[4 * c + j], p[0][1], p[1][1], p[0][0], p[1][0], v[0], v[0]);
     }
   }
 }

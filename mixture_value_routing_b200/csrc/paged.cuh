@@ -130,19 +130,49 @@ __device__ __forceinline__ int clamp_len(int len, int max_pages, int shift) {
   return len < 0 ? 0 : (len > cap ? static_cast<int>(cap) : len);
 }
 
+// c (16 x 8, fp32) += a (16 x 16) b (16 x 8), both bf16 or both fp16 (kHalf).
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (!kHalf)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Two E4M3 values (low 16 bits of x, or high) as fp16, exactly.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
 // Prepares `kern` for its launches, once per device: `bytes` of dynamic shared
-// memory, and the SM's memory split all to shared memory.  Kernels chained by
-// programmatic dependent launch overlap, and an SM changes its split only when
-// idle: one kernel with another split would keep the next one's CTAs off.
+// memory, and the SM's memory split all to shared memory unless `carveout` says
+// otherwise.  Kernels chained by programmatic dependent launch overlap, and an SM
+// changes its split only when idle: a kernel with another split keeps the next
+// one's CTAs off.
 template <typename K>
-cudaError_t prepare_kernel(K kern, size_t bytes, bool (&done)[64]) {
+cudaError_t prepare_kernel(K kern, size_t bytes, bool (&done)[64], int carveout = cudaSharedmemCarveoutMaxShared) {
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
   if (err == cudaSuccess)
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, carveout);
   if (err == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
   return err;
 }

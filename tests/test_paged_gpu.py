@@ -476,6 +476,100 @@ def test_select_reports_bad_pages(api):
     assert picked.cpu()[1].tolist() == [[j for j in range(19) if j != 3]] * 2  # counts below every other
 
 
+def repeated(dtype, G, logical, physical, seed=0, kv=2):
+    """One request of `logical` full pages and a last one, over `physical` pages of random bounds."""
+    g = torch.Generator().manual_seed(seed)
+    qt = torch.float32 if dtype == "f32" else torch.bfloat16
+    kt = {"f32": torch.float32, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[dtype]
+    hi = torch.randn(physical, kv, 128, generator=g).to(qt).to(kt)
+    lo = (hi.float() - torch.rand(physical, kv, 128, generator=g)).to(qt).to(kt)
+    q = torch.randn(1, kv * G, 128, generator=g).to(qt)
+    table = torch.randint(physical, (1, logical + 1), generator=g, dtype=I32)
+    return q.cuda(), lo.cuda(), hi.cuda(), table.cuda(), torch.tensor([16 * logical + 1], dtype=I32).cuda()
+
+
+def check_select(api, args, top, status=None):
+    picked = api.page_select(*args, 16, top)
+    ok(api, *([] if status is None else [status]))
+    assert torch.equal(picked.cpu(), P.select(*args, 16, top))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("logical,physical,top", [
+    (3000, 1, 9), (3000, 1, 2900), (600, 500, 200), (40000, 700, 100), (70000, 900, 40000), (33000, 3, 30000),
+])
+def test_select_pages_that_repeat(api, dtype, logical, physical, top):
+    check_select(api, repeated(dtype, 4, logical, physical, seed=top), top)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("G", [1, 5, 16])
+def test_select_scores_that_nearly_agree(api, dtype, G):
+    # Pages that differ by one step in one element, the smallest of the query's: the scores differ
+    # by far less than the rounding of a sum in fp32, and by far more than one in fp64.
+    q, lo, hi, table, lens = repeated(dtype, G, 400, 300, seed=G)
+    q[..., 5] *= 2.0 ** -14
+    lo[:], hi[:] = lo[:1].clone(), hi[:1].clone()
+    raw = {4: torch.int32, 2: torch.int16, 1: torch.int8}[lo.element_size()]
+    for x in (lo, hi):
+        x[:, :, 5] = 1.0
+        x.view(raw)[1::3, :, 5] += 1
+        x.view(raw)[2::3, :, 5] -= 1
+    check_select(api, (q, lo, hi, table, lens), 150)
+    check_select(api, (q, lo, hi, table, lens), 30)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_select_bounds_that_are_not_finite(api, dtype):
+    q, lo, hi, table, lens = repeated(dtype, 1, 900, 901, seed=3, kv=1)
+    table[0] = torch.randperm(901, generator=torch.Generator().manual_seed(4)).to(I32)
+    up, down = (q[0, 0] > 0).nonzero()[:, 0].tolist(), (q[0, 0] < 0).nonzero()[:, 0].tolist()
+    at = table[0].tolist()
+    hi[at[100], 0, up[3]] = math.nan     # a score that is NaN: before all others
+    hi[at[101], 0, down[3]] = math.nan   # an upper bound that the query does not use
+    lo[at[102], 0, up[0]] = math.nan     # and a lower one
+    check_select(api, (q, lo, hi, table, lens), 60)
+    if dtype == "e4m3":
+        return  # no infinities
+    hi[at[200], 0, up[5]] = math.inf     # the greatest
+    lo[at[201], 0, down[5]] = -math.inf  # as great
+    hi[at[202], 0, up[5]] = -math.inf    # the least
+    lo[at[203], 0, up[5]] = -math.inf    # not used
+    check_select(api, (q, lo, hi, table, lens), 60)
+    check_select(api, (q, lo, hi, table, lens), 4)
+    check_select(api, (q, lo, hi, table, lens), 900)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_select_ranges(api, dtype):
+    q, lo, hi, table, lens = repeated(dtype, 4, 2000, 1500, seed=5)
+    check_select(api, (q * 0, lo, hi, table, lens), 50)                    # all scores are zero
+    check_select(api, (q * 2.0 ** -130, lo, hi, table, lens), 50)          # subnormal products
+    check_select(api, (q * 2.0 ** 124, lo, hi, table, lens), 50)           # sums beyond fp32's range
+    q[:, 1] *= 2.0 ** 20                                                   # heads of unlike size
+    check_select(api, (q, lo, hi, table, lens), 50)
+    hi[table[0, 77].item()] = (hi[table[0, 77].item()].float() * 0).to(hi.dtype)
+    lo[table[0, 77].item()] = (lo[table[0, 77].item()].float() * 0).to(lo.dtype)
+    hi[table[0, 78].item()] = (hi[table[0, 78].item()].float() * 64).to(hi.dtype)  # one page far above
+    check_select(api, (q, lo, hi, table, lens), 2)
+    check_select(api, (q, lo, hi, table, lens), 500)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_select_more_pages_than_are_there(api, dtype):
+    q, lo, hi, table, lens = repeated(dtype, 4, 50, 40, kv=1)
+    table[0, [7, 13, 30, 31]] = torch.tensor([-1, 40, -5, 1 << 30], dtype=I32).cuda()
+    picked = api.page_select(q, lo, hi, table, lens, 16, 49)
+    ok(api, ("MOVA_ERR_DEVICE_CHECK", 0))
+    assert picked[0, 0].tolist() == [j for j in range(51) if j not in (30, 31)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_select_more_heads_than_warps(api, dtype):
+    q, lo, hi, table, lens = repeated(dtype, 1, 5, 4, kv=3001)
+    check_select(api, (q, lo, hi, table, lens), 3)
+
+
 # ---- Streams, graphs, repetition -----------------------------------------------------
 
 def test_repeated_calls_are_bit_identical(api):
