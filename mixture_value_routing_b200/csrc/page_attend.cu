@@ -17,7 +17,8 @@
 // the workspace does not grow with the batch.  A worker is a CTA, whose four
 // warps take a tile of each unit (16 keys of bf16, 32 of E4M3, 8 of fp32) and
 // join where a row ends; or, where there are many rows, which may be short, a
-// warp alone, as the joining costs more than a short row.
+// warp alone, as the joining costs more than a short row.  Few rows that cannot
+// be long have a cluster of CTAs each instead, and no second kernel.
 //
 // Stream.  Each warp has a ring of 8 KB stages (K and V of one tile) that it
 // fills with 16-byte asynchronous copies, one or two tiles ahead and across
@@ -44,8 +45,9 @@
 // Measured, of 6459 GB/s: bf16 16 requests to 32768 tokens, 775 MB: 124 us,
 // 97%; 64 x 4096 tokens, 1.1 GB: 168.6 us, 99% with 4 heads, 92% with 16; E4M3
 // 64 requests to 8192, 463 MB: 82 us, 88%; fp32 32 x 4096: 168 us, 99% with 4
-// heads, 73% with 7.  8 requests to 500 tokens: 7.8 us, the latency of two
-// launches and four dependent loads.
+// heads, 73% with 7.  8 requests to 500 tokens: 6.3 us, the latency of a launch
+// and four dependent loads.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include <algorithm>
@@ -57,7 +59,10 @@ namespace mova {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 128;
+constexpr int kMaxCluster = 8;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStageBytes = 8192;  // K and V of one warp's tile
 constexpr int kRingAlign = 256;
@@ -564,9 +569,45 @@ template <int M> __device__ __forceinline__ void store_out(void* o, long long at
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o) + at) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
 }
 
-// NT: mma column tiles of 8 heads, or fp32 heads.
-template <int M, int NT, int kTeam>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_kernel(const AttendArgs s) {
+// What a cluster's CTAs share at the end: unnormalised outputs, then maxima and sums.
+constexpr int kMineFloats = kMaxGroup * kPartRow;
+
+// The status of a call without a second kernel, by one cluster of its own: every
+// length, and every table entry that the other clusters look up.
+__device__ __forceinline__ void check_pages(const AttendArgs& s, StatusBlock* sb, int* sm_bad) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), tid = threadIdx.x, threads = cluster.num_blocks() * kThreads;
+  const int B = s.a.B, kv = s.a.kv, shift = s.a.shift, width = s.picked == nullptr ? s.a.max_pages : s.top;
+  int bad = kNoBad;
+  for (int b = rank * kThreads + tid; b < B; b += threads) {
+    const int len = s.a.lens[b];
+    if (clamp_len(len, s.a.max_pages, shift) != len) bad = min(bad, b);
+  }
+  const int rows = s.picked == nullptr ? B : B * kv;
+#pragma unroll 4
+  for (int i = rank * kThreads + tid; i < rows * width; i += threads) {
+    const int row = i / width, place = i - row * width, b = s.picked == nullptr ? row : row / kv;
+    const int pages = (clamp_len(s.a.lens[b], s.a.max_pages, shift) + (1 << shift) - 1) >> shift;
+    const int page = place >= pages ? -1 : s.picked == nullptr ? place : s.picked[i];
+    if (page >= 0 && page < pages) {
+      const int id = s.a.table[b * s.a.table_stride + page];
+      if (id < 0 || id >= s.a.num_pages) bad = min(bad, b);
+    }
+  }
+  bad = __reduce_min_sync(0xffffffffu, bad);
+  cluster.sync();  // rank 0 has set its word
+  if ((tid & 31) == 0 && bad != kNoBad) atomicMin(cluster.map_shared_rank(sm_bad, 0), bad);
+  cluster.sync();
+  if (rank == 0 && tid == 0) {
+    sb->code = *sm_bad == kNoBad ? MOVA_OK : MOVA_ERR_DEVICE_CHECK;
+    sb->detail = *sm_bad == kNoBad ? 0 : *sm_bad;
+  }
+}
+
+// NT: mma column tiles of 8 heads, or fp32 heads.  kOwn: a cluster has one row,
+// its CTAs equal shares of it, and joins them itself; sb: its status.
+template <int M, int NT, int kTeam, bool kOwn>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_kernel(const AttendArgs s, StatusBlock* sb) {
   using E = typename Tile<M>::E;
   using Out = typename std::conditional<kIsF32<M>, float, __nv_bfloat16>::type;
   constexpr int kKeys = Tile<M>::keys;
@@ -589,19 +630,36 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
   float* q_sm = q_all + (M == kF32 ? warp / kTeam * NT * kHeadDim : 0);
   int* pre = reinterpret_cast<int*>(q_all + (M == kF32 ? kWarps / kTeam * NT * kHeadDim : 0));
 
+  float* mine = reinterpret_cast<float*>(pre);  // kOwn
+
   if (tid == 0) sm_bad = kNoBad;
   pdl_wait();
-  __syncthreads();
-  request_scan<kThreads>(B, pre, [&](int b) {
-    const int len = s.a.lens[b], use = clamp_len(len, s.a.max_pages, shift);
-    if (use != len) atomicMin(&sm_bad, b);
-    return (places_of(s, use) + kUnit - 1) / kUnit;
-  });
-  const int U = kv * pre[B];
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= B; b += kThreads) s.prefix[b] = pre[b];
-  const int w = (blockIdx.x * kWarps + warp) / kTeam, share = share_of<M, kTeam>(gridDim.x, U);
-  const int u0 = min(w * share, U), count = min(share, U - u0);
+  int w = 0, u0, count, row_b = 0, row_h = 0, row_tiles = 0;
+  if constexpr (kOwn) {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = cluster.block_rank(), size = cluster.num_blocks(), id = blockIdx.x / size;
+    if (id == B * kv) {
+      __syncthreads();
+      check_pages(s, sb, &sm_bad);
+      return;
+    }
+    row_b = id / kv, row_h = id - row_b * kv;
+    row_tiles = (places_of(s, clamp_len(s.a.lens[row_b], s.a.max_pages, shift)) + kUnit - 1) / kUnit;
+    u0 = rank * row_tiles / size, count = (rank + 1) * row_tiles / size - u0;
+  } else {
+    __syncthreads();
+    request_scan<kThreads>(B, pre, [&](int b) {
+      const int len = s.a.lens[b], use = clamp_len(len, s.a.max_pages, shift);
+      if (use != len) atomicMin(&sm_bad, b);
+      return (places_of(s, use) + kUnit - 1) / kUnit;
+    });
+    const int U = kv * pre[B];
+    if (blockIdx.x == 0)
+      for (int b = tid; b <= B; b += kThreads) s.prefix[b] = pre[b];
+    const int share = share_of<M, kTeam>(gridDim.x, U);
+    w = (blockIdx.x * kWarps + warp) / kTeam;
+    u0 = min(w * share, U), count = min(share, U - u0);
+  }
 
   // Page lookup of 32 tiles: lane i that of this warp's tile in unit `at + i`,
   // with the row (request, KV head) that it belongs to.
@@ -612,14 +670,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
     for (int j = 0; j < kGroups; ++j) t_page[j] = t_row[j] = t_valid[j] = 0;
     if (i >= count) return;
     const int u = u0 + i;
-    const int b = request_of(pre, B, u / kv);
-    const int tiles = pre[b + 1] - pre[b], rem = u - kv * pre[b];
-    const int h = rem / tiles;
+    int b = row_b, h = row_h, tile = u;
+    if constexpr (!kOwn) {
+      b = request_of(pre, B, u / kv);
+      const int tiles = pre[b + 1] - pre[b], rem = u - kv * pre[b];
+      h = rem / tiles;
+      tile = rem - h * tiles;
+    }
     const int len = clamp_len(s.a.lens[b], s.a.max_pages, shift);
     t_owner = b * kv + h;
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) {
-      const int place = (rem - h * tiles) * kUnit + warp % kTeam * kKeys + 16 * j;
+      const int place = tile * kUnit + warp % kTeam * kKeys + 16 * j;
       const int in = place & ((1 << shift) - 1);
       int page = place >> shift;
       if (s.picked != nullptr) {
@@ -711,10 +773,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
   if (count > 0) {
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
-    int b = request_of(pre, B, u0 / kv);
-    int tiles = pre[b + 1] - pre[b];
-    int h = (u0 - kv * pre[b]) / tiles;
-    int t = u0 - kv * pre[b] - h * tiles;
+    int b = row_b, tiles = row_tiles, h = row_h, t = u0;
+    if constexpr (!kOwn) {
+      b = request_of(pre, B, u0 / kv);
+      tiles = pre[b + 1] - pre[b];
+      h = (u0 - kv * pre[b]) / tiles;
+      t = u0 - kv * pre[b] - h * tiles;
+    }
     State<M, NT> st;
     Query<M, M == kF32 ? 1 : NT> q;
     bool fresh = true, whole = t == 0;
@@ -757,8 +822,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
         // outputs where the tile it has just used was (at most 16 heads x 512
         // bytes; the next copies into that stage start later), to be read back by
         // head: by a warp alone four dimensions a lane, by a team joined.
-        const bool done = whole && row_end;
-        float* part = s.part + (static_cast<size_t>(w) * 2 + (whole ? 1 : 0)) * (G * kPartRow);
+        const bool done = !kOwn && whole && row_end;
+        float* part = kOwn ? mine : s.part + (static_cast<size_t>(w) * 2 + (whole ? 1 : 0)) * (G * kPartRow);
         const long long row = static_cast<long long>(b) * kv + h;
         const float v_scale = M == kE8 && s.a.v_scale != nullptr ? s.a.v_scale[h] : 1.0f;
         float* turn = reinterpret_cast<float*>(tile);
@@ -892,6 +957,43 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
     }
     cp_wait<0>();
   }
+  if constexpr (kOwn) {
+    // The cluster's CTAs take the heads in turn, a thread a dimension.
+    cg::cluster_group cluster = cg::this_cluster();
+    const int size = cluster.num_blocks();
+    if (count == 0)
+      for (int head = 0; head < G; ++head) {
+        mine[head * kHeadDim + tid] = 0.0f;
+        if (tid == 0) mine[G * kHeadDim + head] = -INFINITY, mine[G * (kHeadDim + 1) + head] = 0.0f;
+      }
+    cluster.sync();
+    const long long row = static_cast<long long>(row_b) * kv + row_h;
+    for (int head = cluster.block_rank(); head < G; head += size) {
+      float pm[kMaxCluster], pl[kMaxCluster], po[kMaxCluster], m = -INFINITY, l = 0.0f, o = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kMaxCluster; ++x) {
+        pm[x] = -INFINITY, pl[x] = po[x] = 0.0f;
+        if (x < size) {
+          const float* part = cluster.map_shared_rank(mine, x);
+          pm[x] = part[G * kHeadDim + head];
+          pl[x] = part[G * (kHeadDim + 1) + head];
+          po[x] = part[head * kHeadDim + tid];
+        }
+        m = fmaxf(m, pm[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < kMaxCluster; ++x) {
+        const float f = ex2(pm[x] - ref_of(m));
+        l = fmaf(pl[x], f, l);
+        o = fmaf(po[x], f, o);
+      }
+      static_cast<Out*>(s.o)[(row * G + head) * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : o / l);
+      if (tid == 0 && s.lse != nullptr) s.lse[row * G + head] = (m + log2f(l)) * kLn2;
+    }
+    pdl_trigger();
+    cluster.sync();  // nobody leaves while its part may be read
+    return;
+  }
   // Only now: CTAs of the join that wait on an SM from the start cost this
   // kernel a third of its rate (118 us against 83 for 463 MB of E4M3 pages).
   pdl_trigger();
@@ -990,9 +1092,64 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
         (m + log2f(l)) * kLn2);
 }
 
+// Tokens of a row that may be attended, by the host's knowledge.
+long long row_tokens(const AttendArgs& s) {
+  const long long pages = s.picked == nullptr ? s.a.max_pages : std::min(s.top, s.a.max_pages);
+  return pages << s.a.shift;
+}
+
+// One launch, a cluster to a row: for calls that have few rows, all of whose
+// clusters are resident, and whose rows cannot be long.  It saves the second
+// launch and the partial results' way through memory, about 2.5 us and as much
+// of the host's time, and loses where lengths differ, as one cluster may then
+// have what all would share.  So a CTA has at most kOwnBytes, which it reads in
+// about 4 us; twice that of picked pages, of which every long row has the same
+// number, unless they are fp32, whose products take longer than their bytes.
+// Measured, one launch and two: bf16, 8 KV heads, 8 requests of 250 tokens 5.6
+// and 8.6 us, 8 of 2000 14.9 and 18.8, 1 of 4000 8.8 and 10.0, 1 of 8000 13.2
+// and 12.1; fp32 with 7 heads a KV head, 5 of 3001 29 and 24.  Clusters of 16
+// gained 0.7 us for one request of 4000 and lost 0.8 for one of 500.  False: the
+// call is not one for it.
+constexpr long long kOwnBytes = 256 << 10;
+template <int M, int NT>
+bool launch_own(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, cudaError_t* err) {
+  constexpr int kUnit = kWarps * Tile<M>::keys, kKeyBytes = 2 * kHeadDim * sizeof(typename Tile<M>::E);
+  constexpr size_t kSmem = attend_smem<M, NT, kWarps>(0) + kMineFloats * 4;
+  const long long rows = static_cast<long long>(s.a.B) * s.a.kv, units = (row_tokens(s) + kUnit - 1) / kUnit;
+  const long long resident = static_cast<long long>(sm_count()) * ctas_per_sm<M, NT>();
+  int size = 1;
+  while (size < kMaxCluster && (rows + 1) * size * 2 <= resident && size < units) size *= 2;
+  const long long own = s.picked != nullptr && !kIsF32<M> ? 2 * kOwnBytes : kOwnBytes;
+  // What one cluster checks for the status, 32 table entries a thread at most.
+  const long long entries = s.picked == nullptr ? static_cast<long long>(s.a.B) * s.a.max_pages : rows * s.top;
+  if ((rows + 1) * size > resident || (units + size - 1) / size * kUnit * kKeyBytes > own ||
+      entries > size * kThreads * 32)
+    return false;
+  auto kern = page_attend_kernel<M, NT, kWarps, true>;
+  static bool done[64] = {false};
+  *err = prepare_kernel(kern, kSmem, done);
+  if (*err != cudaSuccess) return true;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 1) * size));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = size;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  note_launch();
+  *err = cudaLaunchKernelEx(&cfg, kern, s, sb);
+  return true;
+}
+
 template <int M, int NT, int kTeam>
 cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
-  auto kern = page_attend_kernel<M, NT, kTeam>;
+  auto kern = page_attend_kernel<M, NT, kTeam, false>;
   static bool done[64] = {false};
   cudaError_t err = prepare_kernel(kern, attend_smem<M, NT, kTeam>(kMaxRequests), done);
   if (err != cudaSuccess) return err;
@@ -1000,12 +1157,10 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   // All CTAs are resident at once, as each takes an equal share.
   const int per_sm = std::max(1, std::min(ctas_per_sm<M, NT>(), static_cast<int>((227 * 1024) / (smem + 2048))));
   constexpr int kCta = kWarps * kLeast<M, kTeam> * Tile<M>::keys;  // tokens that keep a CTA busy
-  const long long tokens = s.picked == nullptr ? static_cast<long long>(s.a.max_pages) << s.a.shift
-                                               : static_cast<long long>(std::min(s.top, s.a.max_pages)) << s.a.shift;
-  const long long most = static_cast<long long>(s.a.B) * s.a.kv * ((tokens + kCta - 1) / kCta);
+  const long long most = static_cast<long long>(s.a.B) * s.a.kv * ((row_tokens(s) + kCta - 1) / kCta);
   const int ctas = static_cast<int>(std::max(1LL, std::min({static_cast<long long>(sm_count()) * per_sm, most,
                                                              static_cast<long long>(kMaxCtas)})));
-  err = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, s);
+  err = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, s, sb);
   if (err != cudaSuccess) return err;
   // Few rows have many parts each, and leave SMs free: a CTA per head.
   const int rows = s.a.B * s.a.kv;
@@ -1028,6 +1183,8 @@ constexpr int kAloneRows = 1024;
 
 template <int M, int NT>
 cudaError_t launch_attend(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
+  cudaError_t err = cudaSuccess;
+  if (launch_own<M, NT>(s, sb, stream, &err)) return err;
   return static_cast<long long>(s.a.B) * s.a.kv >= kAloneRows ? launch_attend_t<M, NT, 1>(s, sb, stream)
                                                               : launch_attend_t<M, NT, kWarps>(s, sb, stream);
 }

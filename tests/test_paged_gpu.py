@@ -274,6 +274,36 @@ def test_attend_lengths(api, dtype, lens, kv, G, page):
     check_attend(api, P.make(dtype, lens, kv, G, page, seed=len(lens)), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("kv,G,page", [(1, 1, 16), (8, 4, 32), (3, 7, 128), (2, 16, 256), (5, 2, 16)])
+@pytest.mark.parametrize("tokens", [512, 4096, 100000])
+def test_attend_table_widths(api, dtype, kv, G, page, tokens):
+    """The same short rows, where the table could hold few tokens each, and many."""
+    lens = EDGES[::2] if kv < 4 else [500, 0, 64]
+    check_attend(api, P.make(dtype, lens, kv, G, page, seed=kv + G, width=tokens // page), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("tokens", [512, 60000])
+@pytest.mark.parametrize("pick", [False, True])
+def test_attend_reports_the_first_bad_request(api, dtype, tokens, pick):
+    s = P.make(dtype, [130] * 40, 2, 4, 16, width=tokens // 16)
+    picked = torch.arange(1, 9, dtype=I32).repeat(40, 2, 1).cuda() if pick else None  # not page 0
+    s["table"][35, 4], s["table"][21, 8], s["table"][9, 0] = -1, s["k"].shape[0], 1 << 30
+    want = 21 if pick else 9
+    check_attend(api, s, dtype, picked=picked, status=("MOVA_ERR_DEVICE_CHECK", want))
+    s["lens"][3] = 1 << 30
+    api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], picked=picked, k_scale=s["ks"], v_scale=s["vs"])
+    ok(api, ("MOVA_ERR_DEVICE_CHECK", 3))
+    s["lens"][3] = -1
+    api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], picked=picked, k_scale=s["ks"], v_scale=s["vs"])
+    ok(api, ("MOVA_ERR_DEVICE_CHECK", 3))
+    s["lens"][3] = 130
+    s["table"][[35, 21, 9], [4, 8, 0]] = 0
+    api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], picked=picked, k_scale=s["ks"], v_scale=s["vs"])
+    ok(api)
+
+
 def test_attend_many_requests(api):
     lens = [(7 * i) % 23 for i in range(4096)]
     check_attend(api, P.make("bf16", lens, 1, 2, 16), "bf16")
