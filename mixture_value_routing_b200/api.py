@@ -15,7 +15,9 @@ Every function enqueues on torch's current CUDA stream (the host-buffer forms:
 on `stream` if given) and returns without synchronising.  Device-side checks
 are read with get_status().  A call given no `ws` uses the workspace this
 module keeps for its device and stream, so calls on different streams may
-overlap on the GPU.  Calls that share a `ws` must run on one stream.
+overlap on the GPU.  Calls that share a `ws` must run on one stream.  A paged
+call that a graph captures without a `ws` has one in the graph's own memory,
+whose status get_status() does not read: give it a `ws` to read one.
 """
 from __future__ import annotations
 
@@ -803,7 +805,7 @@ def arm_stream_stall(stall_stage: int, limit_cycles: int) -> None:
 
 
 def get_status(ws: Optional[torch.Tensor] = None, device=None, stream=None):
-    """(status name, detail) of the last value call on this workspace; without
+    """(status name, detail) of the last call on this workspace; without
     `ws`, on the default workspace of `stream` (else of the current stream),
     i.e. of the last call made there without `ws`.  Waits for that stream."""
     if ws is None:
