@@ -17,8 +17,9 @@
 // the workspace does not grow with the batch.  A worker is a CTA, whose four
 // warps take a tile of each unit (16 keys of bf16, 32 of E4M3, 8 of fp32) and
 // join where a row ends; or, where there are many rows, which may be short, a
-// warp alone, as the joining costs more than a short row.  Few rows that cannot
-// be long have a cluster of CTAs each instead, and no second kernel.
+// warp alone, as the joining costs more than a short row.  Rows that cannot be
+// long are instead a cluster's each, where they are few, or a warp's, without
+// scan, partial results or second kernel.
 //
 // Stream.  Each warp has a ring of 8 KB stages (K and V of one tile) that it
 // fills with 16-byte asynchronous copies, one or two tiles ahead and across
@@ -605,7 +606,8 @@ __device__ __forceinline__ void check_pages(const AttendArgs& s, StatusBlock* sb
 }
 
 // NT: mma column tiles of 8 heads, or fp32 heads.  kOwn: a cluster has one row,
-// its CTAs equal shares of it, and joins them itself; sb: its status.
+// its CTAs equal shares of it, and joins them itself (a team), or a warp has one
+// (kTeam = 1); the first cluster sees to the status, sb.
 template <int M, int NT, int kTeam, bool kOwn>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_kernel(const AttendArgs s, StatusBlock* sb) {
   using E = typename Tile<M>::E;
@@ -637,15 +639,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
   int w = 0, u0, count, row_b = 0, row_h = 0, row_tiles = 0;
   if constexpr (kOwn) {
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = cluster.block_rank(), size = cluster.num_blocks(), id = blockIdx.x / size;
-    if (id == B * kv) {
+    const int rank = cluster.block_rank(), size = cluster.num_blocks(), id = blockIdx.x / size - 1;
+    if (id < 0) {
       __syncthreads();
       check_pages(s, sb, &sm_bad);
       return;
     }
-    row_b = id / kv, row_h = id - row_b * kv;
+    const int row = kTeam > 1 ? id : (id * size + rank) * kWarps + warp;
+    if (kTeam == 1 && row >= B * kv) return;
+    row_b = row / kv, row_h = row - row_b * kv;
     row_tiles = (places_of(s, clamp_len(s.a.lens[row_b], s.a.max_pages, shift)) + kUnit - 1) / kUnit;
-    u0 = rank * row_tiles / size, count = (rank + 1) * row_tiles / size - u0;
+    u0 = kTeam > 1 ? rank * row_tiles / size : 0;
+    count = kTeam > 1 ? (rank + 1) * row_tiles / size - u0 : row_tiles;
   } else {
     __syncthreads();
     request_scan<kThreads>(B, pre, [&](int b) {
@@ -822,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
         // outputs where the tile it has just used was (at most 16 heads x 512
         // bytes; the next copies into that stage start later), to be read back by
         // head: by a warp alone four dimensions a lane, by a team joined.
-        const bool done = !kOwn && whole && row_end;
+        const bool done = kOwn ? kTeam == 1 : whole && row_end;
         float* part = kOwn ? mine : s.part + (static_cast<size_t>(w) * 2 + (whole ? 1 : 0)) * (G * kPartRow);
         const long long row = static_cast<long long>(b) * kv + h;
         const float v_scale = M == kE8 && s.a.v_scale != nullptr ? s.a.v_scale[h] : 1.0f;
@@ -956,6 +961,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
       ++t;
     }
     cp_wait<0>();
+  }
+  if constexpr (kOwn && kTeam == 1) {
+    if (count == 0) {
+      const long long row = static_cast<long long>(row_b) * kv + row_h;
+      for (int head = 0; head < G; ++head) {
+        store_out<M>(s.o, (row * G + head) * kHeadDim + 4 * lane, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+        if (lane == 0 && s.lse != nullptr) s.lse[row * G + head] = -INFINITY;
+      }
+    }
+    pdl_trigger();
+    return;
   }
   if constexpr (kOwn) {
     // The cluster's CTAs take the heads in turn, a thread a dimension.
@@ -1092,10 +1108,39 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
         (m + log2f(l)) * kLn2);
 }
 
+// Rows from which warps work alone.  Measured on bf16: 8192 rows of 100 tokens
+// 135 us alone, 212 in teams; 512 rows of 4096 171 and 169; 64 rows to 500
+// 13.2 and 7.7.
+constexpr int kAloneRows = 1024;
+
 // Tokens of a row that may be attended, by the host's knowledge.
 long long row_tokens(const AttendArgs& s) {
   const long long pages = s.picked == nullptr ? s.a.max_pages : std::min(s.top, s.a.max_pages);
   return pages << s.a.shift;
+}
+
+template <int M, int NT, int kTeam>
+cudaError_t launch_clusters(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, long long clusters, int size,
+                            size_t smem) {
+  auto kern = page_attend_kernel<M, NT, kTeam, true>;
+  static bool done[64] = {false};
+  cudaError_t err = prepare_kernel(kern, smem, done);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * size));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = size;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kern, s, sb);
 }
 
 // One launch, a cluster to a row: for calls that have few rows, all of whose
@@ -1125,28 +1170,33 @@ bool launch_own(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, cudaE
   if ((rows + 1) * size > resident || (units + size - 1) / size * kUnit * kKeyBytes > own ||
       entries > size * kThreads * 32)
     return false;
-  auto kern = page_attend_kernel<M, NT, kWarps, true>;
-  static bool done[64] = {false};
-  *err = prepare_kernel(kern, kSmem, done);
-  if (*err != cudaSuccess) return true;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 1) * size));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = size;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  note_launch();
-  *err = cudaLaunchKernelEx(&cfg, kern, s, sb);
+  *err = launch_clusters<M, NT, kWarps>(s, sb, stream, rows + 1, size, kSmem);
   return true;
 }
 
+// One launch, a warp to a row: where clusters would not all be resident and rows
+// cannot be long.  CTAs come and go, so that many short rows need no scan of the
+// lengths (whose place in shared memory leaves one CTA an SM for 4096 requests),
+// no partial results and no second kernel.  A row may have kWarpBytes, which a
+// warp reads in about 8 us; twice that of 1024 rows or more, where the last rows
+// are a small part of the time, but not of fp32, whose rows take longer.
+// Measured, one launch and two: bf16 8192 rows of 100 tokens 87 and 137 us, of
+// 20 43 and 71; 512 of 200 14.7 and 17.3; 1024 of 400 37 and 42; 640 to 500 26
+// and 23; E4M3 1024 of 200 13 and 19, 2048 of 400 50 and 47; fp32 8192 of 100
+// 164 and 173, 2048 of 200 98 and 78.  False: the call is not one for it.
+constexpr long long kWarpBytes = 128 << 10;
+template <int M, int NT>
+bool launch_warps(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, cudaError_t* err) {
+  constexpr int kKeyBytes = 2 * kHeadDim * sizeof(typename Tile<M>::E);
+  const long long rows = static_cast<long long>(s.a.B) * s.a.kv;
+  const long long entries = s.picked == nullptr ? static_cast<long long>(s.a.B) * s.a.max_pages : rows * s.top;
+  const long long most = rows >= kAloneRows && !kIsF32<M> ? 2 * kWarpBytes : kWarpBytes;
+  if (row_tokens(s) * kKeyBytes > most || entries > kMaxCluster * kThreads * 64) return false;
+  constexpr int kRows = kMaxCluster * kWarps;
+  *err = launch_clusters<M, NT, 1>(s, sb, stream, (rows + kRows - 1) / kRows + 1, kMaxCluster,
+                                   attend_smem<M, NT, 1>(0));
+  return true;
+}
 template <int M, int NT, int kTeam>
 cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
   auto kern = page_attend_kernel<M, NT, kTeam, false>;
@@ -1176,15 +1226,11 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   return launch_pdl(page_join_kernel<M, kTeam, 1>, dim3(rows), dim3(32 * s.G), 0, stream, s, ctas, sb);
 }
 
-// Rows from which warps work alone.  Measured on bf16: 8192 rows of 100 tokens
-// 135 us alone, 212 in teams; 512 rows of 4096 171 and 169; 64 rows to 500
-// 13.2 and 7.7.
-constexpr int kAloneRows = 1024;
-
 template <int M, int NT>
 cudaError_t launch_attend(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
   cudaError_t err = cudaSuccess;
   if (launch_own<M, NT>(s, sb, stream, &err)) return err;
+  if (launch_warps<M, NT>(s, sb, stream, &err)) return err;
   return static_cast<long long>(s.a.B) * s.a.kv >= kAloneRows ? launch_attend_t<M, NT, 1>(s, sb, stream)
                                                               : launch_attend_t<M, NT, kWarps>(s, sb, stream);
 }

@@ -284,11 +284,29 @@ def test_attend_table_widths(api, dtype, kv, G, page, tokens):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("kv,G,page", [(1, 16, 16), (7, 4, 32), (2, 9, 64)])
+@pytest.mark.parametrize("tokens", [256, 40000])
+def test_attend_many_short_rows(api, dtype, kv, G, page, tokens):
+    """More rows than CTAs fit, some empty, where the table could hold few tokens each, and many."""
+    lens = [(37 * i) % 131 if i % 5 else 0 for i in range(1203 // kv)]
+    check_attend(api, P.make(dtype, lens, kv, G, page, seed=kv, width=tokens // page), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+def test_attend_many_rows_of_picked_pages(api, dtype):
+    s = P.make(dtype, [(41 * i) % 190 for i in range(600)], 2, 4, 16, seed=8)
+    picked = (torch.arange(600 * 2 * 4).view(600, 2, 4) * 7 % 13).to(I32)
+    picked[::9] = -1
+    check_attend(api, s, dtype, picked=picked.cuda())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
 @pytest.mark.parametrize("tokens", [512, 60000])
 @pytest.mark.parametrize("pick", [False, True])
-def test_attend_reports_the_first_bad_request(api, dtype, tokens, pick):
-    s = P.make(dtype, [130] * 40, 2, 4, 16, width=tokens // 16)
-    picked = torch.arange(1, 9, dtype=I32).repeat(40, 2, 1).cuda() if pick else None  # not page 0
+@pytest.mark.parametrize("rows", [40, 700])
+def test_attend_reports_the_first_bad_request(api, dtype, tokens, pick, rows):
+    s = P.make(dtype, [130] * 40 + [3] * (rows - 40), 2, 4, 16, width=(tokens if rows == 40 else tokens // 2) // 16)
+    picked = torch.arange(1, 9, dtype=I32).repeat(rows, 2, 1).cuda() if pick else None  # not page 0
     s["table"][35, 4], s["table"][21, 8], s["table"][9, 0] = -1, s["k"].shape[0], 1 << 30
     want = 21 if pick else 9
     check_attend(api, s, dtype, picked=picked, status=("MOVA_ERR_DEVICE_CHECK", want))
