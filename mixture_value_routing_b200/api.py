@@ -739,7 +739,9 @@ def page_attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, t
     """Attention of one new token per request over its cached tokens
     (mova_page_attend): o (B, H, 128) in q's dtype [, lse (B, H) fp32], zeros
     (and -inf) for requests of length 0.  scale defaults to 1 / sqrt(128).
-    picked (B, KV heads, top): only these pages, from page_select."""
+    picked (B, KV heads, top): only these pages, from page_select.  The width
+    of `table` bounds the lengths that the call is laid out for: a table no
+    wider than the longest request needs is fastest."""
     if _elsewhere(q):
         with torch.cuda.device(q.device):
             return page_attend(q, k_cache, v_cache, table, lens, scale, picked, k_scale, v_scale, return_lse, out, ws)
