@@ -322,6 +322,12 @@ def test_attend_reports_the_first_bad_request(api, dtype, tokens, pick, rows):
     ok(api)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("lens,kv,G", [([30011], 1, 16), ([30011], 1, 1), ([20000, 0, 777], 1, 5), ([9000, 8000], 2, 8)])
+def test_attend_rows_of_many_parts(api, dtype, lens, kv, G):
+    check_attend(api, P.make(dtype, lens, kv, G, 64, seed=G), dtype)
+
+
 def test_attend_many_requests(api):
     lens = [(7 * i) % 23 for i in range(4096)]
     check_attend(api, P.make("bf16", lens, 1, 2, 16), "bf16")
