@@ -40,13 +40,14 @@
 // rate is enough for 8 bytes per token, head and dimension.  fp32, more heads:
 // the FMAs and their operands from shared memory would bound it (16 heads: 470
 // us for 1.1 GB), so every fp32 number is split exactly into three bf16 parts
-// and six products of parts are formed by mma (225 us); there an infinite key
-// or value shows as NaN.
+// and six products of parts are formed by mma (217 us; up to 8 heads, two parts
+// at a time in the rows that heads leave free, 169 us); there an infinite key or
+// value shows as NaN.
 //
 // Measured, of 6459 GB/s: bf16 16 requests to 32768 tokens, 775 MB: 124 us,
 // 97%; 64 x 4096 tokens, 1.1 GB: 168.6 us, 99% with 4 heads, 92% with 16; E4M3
-// 64 requests to 8192, 463 MB: 82 us, 88%; fp32 32 x 4096: 168 us, 99% with 4
-// heads, 73% with 7.  8 requests to 500 tokens: 6.3 us, the latency of a launch
+// 64 requests to 8192, 463 MB: 82 us, 88%; fp32 32 x 4096: 164 us, 101% with 4
+// heads, 98% with 7, 77% with 16.  8 requests to 500 tokens: 6.3 us, the latency of a launch
 // and four dependent loads.
 #include <cooperative_groups.h>
 #include <math.h>
@@ -432,10 +433,11 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t (&p)[3]) {
 // fp32 by parts: heads g and g + 8 (NT = 2) of the rows of S = q K^T and
 // O = P V.  Output tile 4 c + j holds dimensions 32 c + 4 n + j in column n, so
 // a lane's columns 2 t and 2 t + 1 of tiles 4 c .. 4 c + 3 are dimensions
-// 32 c + 8 t .. + 7.
+// 32 c + 8 t .. + 7.  NT = 1: rows g + 8 have what the second part of P gives.
 template <int NT> struct State<kF32Parts, NT> {
   float o[16][4];
   float m[2], l[2];
+  __device__ __forceinline__ float at(int tile, int i) const { return NT > 1 ? o[tile][i] : o[tile][i] + o[tile][i + 2]; }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -474,27 +476,46 @@ template <int NT>
 __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Query<kF32Parts, NT>& q, float scale,
                                                const char* kt, const char* vt, int valid, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  float s[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+  // Several sums, as a product waits for the one before it in its sum.
+  constexpr int kSums = NT > 1 ? 3 : 4;
+  float s[kSums][4];
+#pragma unroll
+  for (int i = 0; i < kSums; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const float4 x = *reinterpret_cast<const float4*>(kt + g * 512 + (((4 * k + t) ^ f32_swizzle(g)) << 4));
     uint32_t lo[3], hi[3];
     split3(x.x, x.y, lo);
     split3(x.z, x.w, hi);
-    // The small pairs first, apart from the large one.
+    if constexpr (NT > 1) {
+      // By the size of the pairs.
 #pragma unroll
-    for (int sum = 2; sum >= 0; --sum)
+      for (int sum = 2; sum >= 0; --sum)
 #pragma unroll
-      for (int i = 0; i <= sum; ++i)
-        mma16816<false>(s[sum == 0 ? 0 : 1], q.a[i][k][0], NT > 1 ? q.a[i][k][NT - 1] : 0u, q.a[i][k][NT],
-                       NT > 1 ? q.a[i][k][2 * NT - 1] : 0u, lo[sum - i], hi[sum - i]);
+        for (int i = 0; i <= sum; ++i)
+          mma16816<false>(s[sum], q.a[i][k][0], q.a[i][k][NT - 1], q.a[i][k][NT], q.a[i][k][2 * NT - 1], lo[sum - i],
+                          hi[sum - i]);
+    } else {
+      // The rows that no head has take the second part of q.
+      mma16816<false>(s[3], q.a[2][k][0], 0u, q.a[2][k][1], 0u, lo[0], hi[0]);
+#pragma unroll
+      for (int i = 2; i >= 0; --i)
+        mma16816<false>(s[i], q.a[0][k][0], q.a[1][k][0], q.a[0][k][1], q.a[1][k][1], lo[i], hi[i]);
+    }
   }
-  uint32_t p[2][3];  // parts of P: heads g and g + 8, keys 2t, 2t + 1
+  // Score of keys 2 t + c, head g + 8 r: the small pairs first.
+  auto score = [&](int r, int c) {
+    if constexpr (NT > 1)
+      return (s[2][2 * r + c] + s[1][2 * r + c]) + s[0][2 * r + c];
+    else
+      return ((((s[2][2 + c] + s[3][c]) + s[2][c]) + s[1][2 + c]) + (s[0][2 + c] + s[1][c])) + s[0][c];
+  };
+  uint32_t p[NT][3];  // parts of P: heads g (and g + 8), keys 2t, 2t + 1
 #pragma unroll
   for (int r = 0; r < NT; ++r) {
     float x[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) x[c] = 2 * t + c < valid ? (s[0][2 * r + c] + s[1][2 * r + c]) * scale : -INFINITY;
+    for (int c = 0; c < 2; ++c) x[c] = 2 * t + c < valid ? score(r, c) * scale : -INFINITY;
     float top = fmaxf(x[0], x[1]);
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -503,7 +524,9 @@ __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Q
       const float a = ex2(st.m[r] - ref_of(m));
       st.l[r] *= a;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) st.o[i][2 * r] *= a, st.o[i][2 * r + 1] *= a;
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int c = NT > 1 ? 2 * r : 0; c < (NT > 1 ? 2 * r + 2 : 4); ++c) st.o[i][c] *= a;
     }
     st.m[r] = m;
 #pragma unroll
@@ -511,7 +534,6 @@ __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Q
     st.l[r] += x[0] + x[1];
     split3(x[0], x[1], p[r]);
   }
-  if (NT == 1) p[1][0] = p[1][1] = p[1][2] = 0u;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const float4 x = *reinterpret_cast<const float4*>(vt + 2 * t * 512 + (((8 * c + g) ^ f32_swizzle(2 * t)) << 4));
@@ -521,10 +543,16 @@ __device__ __forceinline__ void tile_f32_parts(State<kF32Parts, NT>& st, const Q
     for (int j = 0; j < 4; ++j) {
       uint32_t v[3];
       split3(xs[j], ys[j], v);
-      // Two pairs of parts at a time, one in each half of the 16 keys' places.
-      mma16816<false>(st.o[4 * c + j], p[0][0], p[1][0], p[0][1], p[1][1], v[2], v[1]);
-      mma16816<false>(st.o[4 * c + j], p[0][2], p[1][2], p[0][0], p[1][0], v[0], v[1]);
-      mma16816<false>(st.o[4 * c + j], p[0][1], p[1][1], p[0][0], p[1][0], v[0], v[0]);
+      // Two pairs of parts at a time, one in each half of the 16 keys' places; and
+      // with the second part of P in the rows that no head has, four.
+      if constexpr (NT > 1) {
+        mma16816<false>(st.o[4 * c + j], p[0][0], p[1][0], p[0][1], p[1][1], v[2], v[1]);
+        mma16816<false>(st.o[4 * c + j], p[0][2], p[1][2], p[0][0], p[1][0], v[0], v[1]);
+        mma16816<false>(st.o[4 * c + j], p[0][1], p[1][1], p[0][0], p[1][0], v[0], v[0]);
+      } else {
+        mma16816<false>(st.o[4 * c + j], p[0][2], 0u, p[0][0], 0u, v[0], v[2]);
+        mma16816<false>(st.o[4 * c + j], p[0][0], p[0][1], p[0][0], p[0][1], v[0], v[1]);
+      }
     }
   }
 }
@@ -889,8 +917,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                   *reinterpret_cast<float4*>(&to[(32 * c + 8 * t4 + 4 * x) ^ z]) =
-                      make_float4(st.o[4 * c][2 * n + x], st.o[4 * c + 1][2 * n + x], st.o[4 * c + 2][2 * n + x],
-                                  st.o[4 * c + 3][2 * n + x]);
+                      make_float4(st.at(4 * c, 2 * n + x), st.at(4 * c + 1, 2 * n + x), st.at(4 * c + 2, 2 * n + x),
+                                  st.at(4 * c + 3, 2 * n + x));
             }
           }
           if constexpr (kTeam == 1) put_all();
@@ -1149,12 +1177,14 @@ cudaError_t launch_clusters(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
 // of the host's time, and loses where lengths differ, as one cluster may then
 // have what all would share.  So a CTA has at most kOwnBytes, which it reads in
 // about 4 us; twice that of picked pages, of which every long row has the same
-// number, unless they are fp32, whose products take longer than their bytes.
+// number; but of fp32 pages, whose products take longer, not that, and half
+// where the clusters leave SMs free.
 // Measured, one launch and two: bf16, 8 KV heads, 8 requests of 250 tokens 5.6
-// and 8.6 us, 8 of 2000 14.9 and 18.8, 1 of 4000 8.8 and 10.0, 1 of 8000 13.2
-// and 12.1; fp32 with 7 heads a KV head, 5 of 3001 29 and 24.  Clusters of 16
-// gained 0.7 us for one request of 4000 and lost 0.8 for one of 500.  False: the
-// call is not one for it.
+// and 8.6 us, 8 of 2000 14.9 and 18.8, 1 of 4000 8.8 and 10.3, 1 of 8000 13.0
+// and 12.2; fp32, 4 of 2000 16.7 and 19.4, 1 of 2000 with one KV head 10.7 and
+// 7.4, 5 to 3001 with 7 heads a KV head 18 and 14.  Clusters of 16 gained 0.7 us
+// for one request of 4000 and lost 0.8 for one of 500.  False: the call is not
+// one for it.
 constexpr long long kOwnBytes = 256 << 10;
 template <int M, int NT>
 bool launch_own(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, cudaError_t* err) {
@@ -1164,7 +1194,8 @@ bool launch_own(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, cudaE
   const long long resident = static_cast<long long>(sm_count()) * ctas_per_sm<M, NT>();
   int size = 1;
   while (size < kMaxCluster && (rows + 1) * size * 2 <= resident && size < units) size *= 2;
-  const long long own = s.picked != nullptr && !kIsF32<M> ? 2 * kOwnBytes : kOwnBytes;
+  const long long own = kIsF32<M> ? (rows * size < sm_count() ? kOwnBytes / 2 : kOwnBytes)
+                                  : (s.picked != nullptr ? 2 * kOwnBytes : kOwnBytes);
   // What one cluster checks for the status, 32 table entries a thread at most.
   const long long entries = s.picked == nullptr ? static_cast<long long>(s.a.B) * s.a.max_pages : rows * s.top;
   if ((rows + 1) * size > resident || (units + size - 1) / size * kUnit * kKeyBytes > own ||
