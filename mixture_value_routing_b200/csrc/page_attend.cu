@@ -9,8 +9,8 @@
 //
 // Split.  The keys of all rows -- a row is a (request, KV head) -- are laid out
 // in one line of units, row by row, and each of the resident workers takes an
-// equal, contiguous share.  Lengths are known on the device only, so every CTA
-// scans them itself.  A worker that covers a row alone writes its output; where
+// equal, contiguous share; empty units stand for what a row's end costs.
+// Lengths are known on the device only, so every CTA scans them itself.  A worker that covers a row alone writes its output; where
 // several share one, each leaves a partial result (running maximum, sum, and
 // unnormalised output) and the second kernel joins them in the order of the
 // keys.  A worker has at most two partial results, its first and its last, so
@@ -46,7 +46,7 @@
 //
 // Measured, of 6459 GB/s: bf16 16 requests to 32768 tokens, 775 MB: 124 us,
 // 97%; 64 x 4096 tokens, 1.1 GB: 168.6 us, 99% with 4 heads, 92% with 16; E4M3
-// 64 requests to 8192, 463 MB: 82 us, 88%; fp32 32 x 4096: 164 us, 101% with 4
+// 64 requests to 8192, 463 MB: 79 us, 91%; fp32 32 x 4096: 164 us, 101% with 4
 // heads, 98% with 7, 77% with 16.  8 requests to 500 tokens: 6.3 us, the latency of a launch
 // and four dependent loads.
 #include <cooperative_groups.h>
@@ -95,6 +95,7 @@ struct AttendArgs {
   int32_t* bad;
   int32_t* prefix;
   float* part;
+  int extra;  // empty units that follow each row's
 };
 
 // Units of request b: of its tokens, or of the picked pages' places.
@@ -648,6 +649,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
   constexpr int kChunks = kRow / 16;
   extern __shared__ char smem_raw[];
   __shared__ float sm_m[kWarps][kMaxGroup], sm_l[kWarps][kMaxGroup];
+  __shared__ float4 sm_f[kTeam > 1 ? kMaxGroup : 1];
+  __shared__ float sm_sum[kTeam > 1 ? kMaxGroup : 1];
   __shared__ int sm_valid[kWarps][kStages][2];
   __shared__ int sm_bad;
 
@@ -684,7 +687,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
     request_scan<kThreads>(B, pre, [&](int b) {
       const int len = s.a.lens[b], use = clamp_len(len, s.a.max_pages, shift);
       if (use != len) atomicMin(&sm_bad, b);
-      return (places_of(s, use) + kUnit - 1) / kUnit;
+      const int tiles = (places_of(s, use) + kUnit - 1) / kUnit;
+      return tiles == 0 ? 0 : tiles + s.extra;
     });
     const int U = kv * pre[B];
     if (blockIdx.x == 0)
@@ -701,14 +705,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
     const int i = at + lane;
 #pragma unroll
     for (int j = 0; j < kGroups; ++j) t_page[j] = t_row[j] = t_valid[j] = 0;
+    t_owner = -1;
     if (i >= count) return;
     const int u = u0 + i;
     int b = row_b, h = row_h, tile = u;
     if constexpr (!kOwn) {
       b = request_of(pre, B, u / kv);
-      const int tiles = pre[b + 1] - pre[b], rem = u - kv * pre[b];
-      h = rem / tiles;
-      tile = rem - h * tiles;
+      const int units = pre[b + 1] - pre[b], rem = u - kv * pre[b];
+      h = rem / units;
+      tile = rem - h * units;
+      if (tile >= units - s.extra) return;  // an empty unit: nothing valid, and no row's
     }
     const int len = clamp_len(s.a.lens[b], s.a.max_pages, shift);
     t_owner = b * kv + h;
@@ -762,6 +768,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
     if ((i & 31) == 0) look_up(i);
     if (i < count) {
       const int owner = __shfl_sync(0xffffffffu, t_owner, i & 31);
+      if (!kOwn && owner < 0) {
+        cp_commit();
+        return;
+      }
       if (owner != ahead) {
         ahead = owner;
         const int line = lane * 128;
@@ -807,16 +817,31 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
     int b = row_b, tiles = row_tiles, h = row_h, t = u0;
+    const int extra = kOwn ? 0 : s.extra;
     if constexpr (!kOwn) {
       b = request_of(pre, B, u0 / kv);
-      tiles = pre[b + 1] - pre[b];
-      h = (u0 - kv * pre[b]) / tiles;
-      t = u0 - kv * pre[b] - h * tiles;
+      const int units = pre[b + 1] - pre[b];
+      tiles = units - extra;
+      h = (u0 - kv * pre[b]) / units;
+      t = u0 - kv * pre[b] - h * units;
     }
     State<M, NT> st;
     Query<M, M == kF32 ? 1 : NT> q;
     bool fresh = true, whole = t == 0;
     for (int i = 0; i < count; ++i) {
+      if (!kOwn && t >= tiles) {  // an empty unit
+        issue(i + kStages - 1);
+        if (++t == tiles + extra) {
+          fresh = whole = true;
+          t = 0;
+          if (i + 1 < count && ++h == kv) {
+            h = 0;
+            do ++b; while (pre[b + 1] == pre[b]);
+            tiles = pre[b + 1] - pre[b] - extra;
+          }
+        }
+        continue;
+      }
       if (fresh) {
         st.clear();
         const long long at = q_at(b * kv + h);
@@ -952,34 +977,46 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
         if constexpr (kTeam == 1) {
           __syncwarp();  // q_sm, sm_m and sm_l are free again
         } else {
-          // A thread joins one dimension of the team's outputs.
+          // A thread a head for the factors, then a thread a dimension for the outputs.
           const float* all = reinterpret_cast<const float*>(smem + stage * kStageBytes);
           constexpr int kNext = kStages * kStageBytes / 4;  // from one warp's stage to the next's
+          static_assert(kTeam == 4, "a head's factors are one float4");
           __syncthreads();
-          for (int head = 0; head < G; ++head) {
-            float m = -INFINITY;
+          if (tid < G) {
+            float m = -INFINITY, f[kTeam], l = 0.0f;
 #pragma unroll
-            for (int x = 0; x < kTeam; ++x) m = fmaxf(m, sm_m[x][head]);
-            float l = 0.0f, o = 0.0f;
+            for (int x = 0; x < kTeam; ++x) m = fmaxf(m, sm_m[x][tid]);
 #pragma unroll
             for (int x = 0; x < kTeam; ++x) {
-              const float f = ex2(sm_m[x][head] - ref_of(m));
-              l = fmaf(sm_l[x][head], f, l);
-              o = fmaf(all[x * kNext + head * kHeadDim + (tid ^ turn_swizzle(head))], f, o);
+              f[x] = ex2(sm_m[x][tid] - ref_of(m));
+              l = fmaf(sm_l[x][tid], f[x], l);
             }
+            sm_f[tid] = make_float4(f[0], f[1], f[2], f[3]);
+            sm_sum[tid] = l;
+            note(tid, m, l);
+          }
+          __syncthreads();
+#pragma unroll 4
+          for (int head = 0; head < G; ++head) {
+            const float4 f = sm_f[head];
+            const float l = sm_sum[head];
+            const float* at = all + head * kHeadDim + (tid ^ turn_swizzle(head));
+            float o = at[0] * f.x;
+            o = fmaf(at[kNext], f.y, o);
+            o = fmaf(at[2 * kNext], f.z, o);
+            o = fmaf(at[3 * kNext], f.w, o);
             o = l == 0.0f ? 0.0f : o * v_scale;
             if (done)
               static_cast<Out*>(s.o)[(row * G + head) * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : o / l);
             else
               part[head * kHeadDim + tid] = o;
-            if (tid == 0) note(head, m, l);
           }
           __syncthreads();
         }
         fresh = whole = true;
-        t = -1;
-        if (row_end && i + 1 < count) {
-          if (++h == kv) {
+        if (row_end && extra == 0) {
+          t = -1;
+          if (i + 1 < count && ++h == kv) {
             h = 0;
             do ++b; while (pre[b + 1] == pre[b]);
             tiles = pre[b + 1] - pre[b];
@@ -1063,7 +1100,7 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / kv, h = blockIdx.x - b * kv;
-  const int p0 = s.prefix[b], tiles = s.prefix[b + 1] - p0, U = kv * s.prefix[B];
+  const int p0 = s.prefix[b], units = s.prefix[b + 1] - p0, tiles = units - s.extra, U = kv * s.prefix[B];
   if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) {
     int bad = kNoBad;
     for (int i = lane; i < ctas; i += 32) bad = min(bad, s.bad[i]);
@@ -1078,11 +1115,11 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
     store_out<M>(s.o, at * kHeadDim + 4 * lane, v);
     if (s.lse != nullptr && lane == 0) s.lse[at] = lse;
   };
-  if (tiles == 0) {
+  if (units == 0) {
     if (group == 0) write(make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY);
     return;
   }
-  const int share = share_of<M, kTeam>(ctas, U), u0 = kv * p0 + h * tiles;
+  const int share = share_of<M, kTeam>(ctas, U), u0 = kv * p0 + h * units;
   const int w0 = u0 / share, parts = (u0 + tiles - 1) / share - w0 + 1;
   if (parts == 1) return;
   const int size = G * kPartRow;
@@ -1266,6 +1303,14 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   return launch_pdl(page_join_kernel<M, kTeam, 1>, dim3(rows), dim3(32 * s.G), 0, stream, s, ctas, sb);
 }
 
+// What ending a row and starting the next costs a worker, in units: rows are laid
+// out that much longer, so that a worker with many short rows has fewer tokens.
+// Measured, without and with: bf16, 512 rows of up to 4096 tokens, 4 heads 78.5
+// and 76.8 us (2: 77.1), 16 heads 100 and 82.7 (1: 92, 2: 85, 8: 82); fp32, 256
+// rows, 7 heads 94 and 81 (1: 86, 4: 82), 16 heads 129 and 106 (2: 107, 8: 111).
+// Rows of one length take the same time either way.
+int row_cost(int G) { return G <= 4 ? 1 : G <= 8 ? 2 : 4; }
+
 template <int M, int NT>
 cudaError_t launch_attend(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream) {
   cudaError_t err = cudaSuccess;
@@ -1280,7 +1325,8 @@ cudaError_t launch_attend(const AttendArgs& s, StatusBlock* sb, cudaStream_t str
 cudaError_t launch_page_attend(const void* q, long long q_stride, int G, const PageArgs& a, mova_dtype dt, float scale,
                                const int32_t* picked, int top, void* o, float* lse, const PageWs& ws,
                                cudaStream_t stream) {
-  const AttendArgs s{a, q, q_stride, G, scale, picked, top, o, lse, ws.bad, ws.prefix, ws.part};
+  const int extra = static_cast<long long>(a.B) * a.kv < (1 << 26) ? row_cost(G) : 0;
+  const AttendArgs s{a, q, q_stride, G, scale, picked, top, o, lse, ws.bad, ws.prefix, ws.part, extra};
   if (dt == MOVA_F32) {
     if (G <= 4) return launch_attend<kF32, 4>(s, ws.sb, stream);
     if (G <= 8) return launch_attend<kF32Parts, 1>(s, ws.sb, stream);

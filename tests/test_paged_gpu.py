@@ -328,6 +328,17 @@ def test_attend_rows_of_many_parts(api, dtype, lens, kv, G):
     check_attend(api, P.make(dtype, lens, kv, G, 64, seed=G), dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("G", [1, 7, 16])
+@pytest.mark.parametrize("seed", range(4))
+def test_attend_uneven_rows_of_a_wide_table(api, dtype, G, seed):
+    """Shares that begin and end at, before and after a row's end."""
+    g = torch.Generator().manual_seed(seed)
+    lens = (torch.randint(400, (50 + 7 * seed,), generator=g) * torch.randint(2, (50 + 7 * seed,), generator=g)).tolist()
+    lens[3] = 2500
+    check_attend(api, P.make(dtype, lens, 3 + seed, G, 32, seed=seed, width=1500), dtype)
+
+
 def test_attend_many_requests(api):
     lens = [(7 * i) % 23 for i in range(4096)]
     check_attend(api, P.make("bf16", lens, 1, 2, 16), "bf16")
