@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectArgs s,
 
   // 0: not among the K greatest; 1: among them; 2: unsure.
   float from = 0.0f, above = 0.0f;
-  auto judge = [&](float z) { return z < from || z == -INFINITY ? 0 : z > above ? 1 : 2; };
+  auto side_of = [&](float z) { return z < from || z == -INFINITY ? 0 : z > above ? 1 : 2; };
   // Each warp has a contiguous run of stripes of 32 pages.
   const int stripes = (N + 31) >> 5, span = (stripes + kWarps - 1) / kWarps;
   const int run0 = warp * span, run1 = min(run0 + span, stripes);
@@ -926,7 +926,7 @@ __global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectArgs s,
 
     int sure = 0;
     for (int st = run0; st < run1; ++st) {
-      const int i = 32 * st + lane, at = i < N ? judge(score_of(i)) : 0;
+      const int i = 32 * st + lane, at = i < N ? side_of(score_of(i)) : 0;
       sure += at == 1;
       if (at == 2) {
         const int place = atomicAdd(&sm_unsure, 1);
@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(kThreads) page_pick_kernel(const SelectArgs s,
   int at = __reduce_add_sync(0xffffffffu, lane < warp ? counts[lane] : 0);  // a place for each, in page order
   for (int st = run0; st < run1; ++st) {
     const int i = 32 * st + lane;
-    const bool in = i < N && judge(score_of(i)) == 1;
+    const bool in = i < N && side_of(score_of(i)) == 1;
     const unsigned m = __ballot_sync(0xffffffffu, in);
     if (in) out[at + __popc(m & ((1u << lane) - 1))] = i;
     at += __popc(m);
