@@ -549,6 +549,8 @@ mova_status mova_page_bounds(const mova_pages* pages, const int32_t* table, long
  * Of each list the first min(top, pages of the request) entries are read;
  * one that is no page of the request (-1) is skipped; one given twice counts
  * twice.  Lengths are clamped to [0, max_pages * page_size] and reported.
+ * With E4M3 pages a weight p_i enters the sum over v_i rounded to 2^-11 of
+ * itself, or to 2^-40 of the greatest, whichever is more.
  * NaN and infinite keys or values that count show in o as the formula has it,
  * except that with fp32 pages and more than 4 query heads to a KV head an
  * infinite one shows as NaN. */

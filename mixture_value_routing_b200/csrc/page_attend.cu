@@ -35,8 +35,10 @@
 // (p = hi + lo, relative error 2^-16): one term would add an error as large
 // as the output's own rounding.  E4M3: K, V become fp16 exactly; q is scaled
 // by a power of two to [1, 2) at its largest element and rounded to fp16
-// (exact for elements down to 2^-14 of the largest); P in fp16 (2^-11 against
-// the output's 2^-8).  fp32, up to 4 query heads a KV head: plain FMAs, whose
+// (exact for elements down to 2^-14 of the largest); P in fp16, 2^15 times as
+// large (kLift), so that weights down to 2^-29 of a warp's greatest keep 2^-11
+// against the output's 2^-8, and only those below 2^-40 count as none.  The sum
+// of the weights is fp32 and as much larger.  fp32, up to 4 query heads a KV head: plain FMAs, whose
 // rate is enough for 8 bytes per token, head and dimension.  fp32, more heads:
 // the FMAs and their operands from shared memory would bound it (16 heads: 470
 // us for 1.1 GB), so every fp32 number is split exactly into three bf16 parts
@@ -131,11 +133,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&p);
 }
-// 2^x for x <= 0 (or NaN), relative error 2^-22; below 2^-126 it is 0.
+// 2^x for x <= 15 (or NaN), relative error 2^-22; below 2^-126 it is 0.
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// The factor of all weights, their sums and outputs: for fp16 weights the greatest
+// power of two that fp16 holds, else 1.  Outputs are quotients, so it shows in
+// the logarithm of a sum only.
+template <int M> constexpr float kLift = M == kE8 ? 0x1p15f : 1.0f;
+template <int M> __device__ __forceinline__ float log_sum(float m, float l) {
+  return (m + log2f(l * (1.0f / kLift<M>))) * kLn2;
 }
 // The maximum to subtract: 0 while nothing has been seen.
 __device__ __forceinline__ float ref_of(float m) { return m == -INFINITY ? 0.0f : m; }
@@ -249,7 +258,11 @@ __device__ __forceinline__ void softmax(State<M, NT>& st, const float (&s)[H][NT
 #pragma unroll
     for (int h = 0; h < H; ++h) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) x[h][c] = ex2(x[h][c] - ref[c & 1]);
+      for (int c = 0; c < 4; ++c) {
+        x[h][c] -= ref[c & 1];
+        if constexpr (M == kE8) x[h][c] += 15.0f;  // after the difference, so that no rounding passes 2^15
+        x[h][c] = ex2(x[h][c]);
+      }
       st.l[n][0] += x[h][0] + x[h][2];
       st.l[n][1] += x[h][1] + x[h][3];
       if constexpr (M == kB16) {
@@ -887,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
         float* turn = reinterpret_cast<float*>(tile);
         auto note = [&](int head, float m, float l) {
           if (done) {
-            if (s.lse != nullptr) s.lse[row * G + head] = (m + log2f(l)) * kLn2;
+            if (s.lse != nullptr) s.lse[row * G + head] = log_sum<M>(m, l);
           } else {
             part[G * kHeadDim + head] = m, part[G * (kHeadDim + 1) + head] = l;
           }
@@ -1069,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<M, NT>()) page_attend_ke
         o = fmaf(po[x], f, o);
       }
       static_cast<Out*>(s.o)[(row * G + head) * kHeadDim + tid] = from_f32<Out>(l == 0.0f ? 0.0f : o / l);
-      if (tid == 0 && s.lse != nullptr) s.lse[row * G + head] = (m + log2f(l)) * kLn2;
+      if (tid == 0 && s.lse != nullptr) s.lse[row * G + head] = log_sum<M>(m, l);
     }
     pdl_trigger();
     cluster.sync();  // nobody leaves while its part may be read
@@ -1170,7 +1183,7 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
   }
   write(make_float4(l == 0.0f ? 0.0f : acc.x / l, l == 0.0f ? 0.0f : acc.y / l, l == 0.0f ? 0.0f : acc.z / l,
                     l == 0.0f ? 0.0f : acc.w / l),
-        (m + log2f(l)) * kLn2);
+        log_sum<M>(m, l));
 }
 
 // Rows from which warps work alone.  Measured on bf16: 8192 rows of 100 tokens

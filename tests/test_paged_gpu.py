@@ -397,6 +397,39 @@ def test_attend_q_of_any_size(api, dtype):
     check_attend(api, s, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("gap", [12.0, 16.0, 17.0, 18.5, 20.0])
+@pytest.mark.parametrize("lens,kv,G,page,width", [
+    ([32, 20, 700], 2, 4, 16, None), ([700, 32], 1, 16, 64, 600), ([30] * 300, 4, 1, 16, None), ([30] * 700, 2, 2, 16, 2000),
+])
+def test_attend_sink_without_a_value(api, dtype, gap, lens, kv, G, page, width):
+    """A first token that outscores all others, which weigh alike, by `gap` and whose
+    value is zero: the output is the others', however small their weights.  Values
+    are not negative and weights alike, so the error is relative to the output:
+    scores off by es (tests/_paged.py; q and keys are whole numbers of every type),
+    2^-21 for the exponential and its argument, one weight's rounding (SPLIT; all
+    are above 2^-29 of the first), fp32 sums of n terms, the output's rounding."""
+    s = P.make(dtype, lens, kv, G, page, seed=int(gap), width=width, fused=False)
+    s["q"], s["ks"] = torch.ones_like(s["q"]), None if s["ks"] is None else torch.ones_like(s["ks"])
+    s["k"] = torch.zeros(s["k"].shape).to(s["k"].dtype).cuda()
+    s["v"] = s["v"].float().nan_to_num(0.0).abs().to(s["v"].dtype)
+    first = s["table"][:, 0].long()
+    s["k"].view(torch.uint8 if dtype == "e4m3" else s["k"].dtype)[first, :, 0] = (
+        torch.ones(1).to(s["k"].dtype).view(torch.uint8).item() if dtype == "e4m3" else 1.0)
+    s["v"].view(torch.uint8 if dtype == "e4m3" else s["v"].dtype)[first, :, 0] = 0
+    scale = gap / 128
+    o, lse = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], scale=scale, k_scale=s["ks"], v_scale=s["vs"],
+                             return_lse=True)
+    ok(api)
+    wo, wl, _, tl = P.attend(s["q"], s["k"], s["v"], s["table"], s["lens"], scale, None,
+                             None if s["ks"] is None else s["ks"].cpu(), None if s["vs"] is None else s["vs"].cpu(), dtype)
+    es = 2 * 130 * P.U * gap
+    tol = P.OUT[dtype] + P.SPLIT[dtype] + 2 * es + 2.0 ** -20 + 4 * max(lens) * P.U
+    err = (P.f64(o) - wo).abs()
+    assert (wo > 0).any() and (err <= tol * wo).all(), (err / wo).nan_to_num(0.0).max()
+    assert ((P.f64(lse) - wl).abs() <= tl).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_attend_nan_and_infinities_show(api, dtype):
     """A NaN or infinite key or value that is attended shows in its heads' outputs,
