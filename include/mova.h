@@ -571,8 +571,9 @@ mova_status mova_page_attend(const void* q, mova_dtype q_dt, long long q_stride,
  * (E4M3: without the head's scale, which changes no order).  q as in
  * mova_page_attend; of `pages` only dtype, num_pages, kv_heads and page_size
  * are read.  picked (B, kv_heads, top) int32 out.  Where some score of a row
- * is not finite, or hundreds lie within rounding of the last one taken, bf16
- * and E4M3 pages take longer: all of the row's pages are scored in fp64. */
+ * is not finite or its products may sum to more than 2^126, or hundreds lie
+ * within rounding of the last one taken, bf16 and E4M3 pages take longer: all
+ * of the row's pages are scored in fp64. */
 mova_status mova_page_select(const void* q, mova_dtype q_dt, long long q_stride, int H, const mova_pages* pages,
                              const void* k_lo, const void* k_hi, const int32_t* table, long long table_stride,
                              int max_pages, const int32_t* lens, int B, int top, int32_t* picked, void* ws,

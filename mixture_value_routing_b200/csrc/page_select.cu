@@ -308,6 +308,9 @@ template <> struct Bound<uint8_t> {
 // 2^-22 of the sums' magnitudes each on the tensor cores: below 2^-17 with the
 // additions within a step; q in fp16 (E4M3) adds 2^-18.  Taken ten times as large.
 constexpr float kScreenError = 0x1p-13f;
+// No sum of products that are below this in all can leave fp32's range, nor a score
+// with its error the range in which the selection steps; others are not screened.
+constexpr float kScreenMost = 0x1p126f;
 
 // NT: tiles of 8 heads.  16 pages (rows) by 8 heads (columns): a lane loads 16
 // bytes a time of pages g and g + 8, whose words are row operands as they are
@@ -472,10 +475,10 @@ __global__ void __launch_bounds__(kScoreThreads, score_per_sm(NT)) page_screen_k
         }
       if (t < 2) {
         const int page = at.page0 + g + 8 * t;
-        const float2 out = (t == 0 ? id0 : id1) < 0
-                               ? make_float2(0.0f, -1.0f)
-                               : make_float2(t == 0 ? best[0] : best[1],
-                                             fmaf(kScreenError * reach, t == 0 ? wide[0] : wide[1], 0x1p-100f));
+        const float far = t == 0 ? wide[0] : wide[1];
+        const float error = reach * far < kScreenMost ? fmaf(kScreenError * reach, far, 0x1p-100f) : INFINITY;
+        const float2 out = (t == 0 ? id0 : id1) < 0 ? make_float2(0.0f, -1.0f)
+                                                    : make_float2(t == 0 ? best[0] : best[1], error);
         if (page < at.pages)
           reinterpret_cast<float2*>(s.keys)[static_cast<long long>(row) * s.a.max_pages + page] = out;
       }

@@ -653,6 +653,32 @@ def test_select_ranges(api, dtype):
     check_select(api, (q, lo, hi, table, lens), 500)
 
 
+def test_select_sums_past_32_bit_floats(api):
+    """Scores that fp32 holds, of sums that it does not: a head whose negative products
+    alone pass 2^128 beside one of a lower, finite score."""
+    lo, hi = torch.zeros(21, 1, 128), torch.zeros(21, 1, 128)
+    j = torch.arange(21.0)[:, None, None] / 256
+    lo[..., :64], hi[..., :64] = (0.5 + j) * 2.0 ** 62, (0.75 + j) * 2.0 ** 62
+    lo[..., 64:] = hi[..., 64:] = 1.0625 * 2.0 ** 62
+    q = torch.zeros(1, 2, 128)
+    q[0, 0, :64], q[0, 0, 64:], q[0, 1, :64] = 2.0 ** 60, -2.0 ** 60, -2.0 ** 60
+    table, lens = ints([list(range(21))]), ints([16 * 20 + 1])
+    q, lo, hi = (x.bfloat16().cuda() for x in (q, lo, hi))
+    want = P.select(q, lo, hi, table, lens, 16, 4)
+    assert want.tolist() == [[[17, 18, 19, 20]]]
+    check_select(api, (q, lo, hi, table, lens), 4)
+
+
+def test_select_scores_next_to_the_greatest_32_bit_float(api):
+    """Equal scores less than their error bound below 2^128."""
+    hi = torch.full((21, 1, 128), 0.99609375 * 2.0 ** 61)
+    q = torch.full((1, 1, 128), 2.0 ** 60)
+    q[..., 5] *= 1.5
+    assert 0.9999 * 2.0 ** 128 < float((q.double() * hi[0].double()).sum()) < 2.0 ** 128
+    q, hi = q.bfloat16().cuda(), hi.bfloat16().cuda()
+    check_select(api, (q, hi, hi, ints([list(range(21))]), ints([16 * 20 + 1])), 4)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
 def test_select_more_pages_than_are_there(api, dtype):
     q, lo, hi, table, lens = repeated(dtype, 4, 50, 40, kv=1)
