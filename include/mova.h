@@ -470,6 +470,8 @@ mova_status mova_value_routed_noalloc(const void* x, mova_dtype x_dt, const floa
  *    the first offending request, or token for mova_page_write).  Nothing is
  *    read or written through a bad page or slot: it counts as absent.
  *  - Requests of length 0 (a padded batch) are valid everywhere.
+ *  - A call of no requests (or of no tokens, mova_page_write) launches nothing
+ *    and may be given no `ws`; one that it is given receives MOVA_OK.
  *  - Results do not depend on timing: no atomics order a sum. */
 typedef struct mova_pages {
   void* k;                  /* (num_pages, kv_heads, page_size, 128) */

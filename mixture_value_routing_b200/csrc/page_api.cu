@@ -1,5 +1,6 @@
 // C ABI entry points of the paged key-value cache: argument checks, workspace
 // layout, and the enqueueing of the kernels on the caller's stream.
+#include <stddef.h>
 #include <stdio.h>
 
 #include "paged.cuh"
@@ -26,6 +27,16 @@ constexpr size_t kStatusBytes = 256;
 
 mova_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
   return ws == nullptr || !aligned(ws, 256) || ws_bytes < need ? MOVA_ERR_INVALID_ARG : MOVA_OK;
+}
+
+// A call of no tokens or requests does nothing but say so in the workspace, if
+// it has one.
+mova_status empty_call(void* ws, size_t ws_bytes, void* stream) {
+  static_assert(MOVA_OK == 0, "the status is set by a memset");
+  if (ws == nullptr) return MOVA_OK;
+  const mova_status st = check_ws(ws, ws_bytes, kStatusBytes);
+  if (st != MOVA_OK) return st;
+  return from_cuda(cudaMemsetAsync(ws, 0, offsetof(StatusBlock, num_active), static_cast<cudaStream_t>(stream)));
 }
 
 int shift_of(int page_size) {
@@ -161,7 +172,7 @@ mova_status mova_page_write(const void* k, const void* v, mova_dtype dt, long lo
   if (st != MOVA_OK) return st;
   if (!io_fits(dt, p.dtype)) return MOVA_ERR_UNSUPPORTED;
   if (T < 0) return MOVA_ERR_INVALID_ARG;
-  if (T == 0) return MOVA_OK;
+  if (T == 0) return empty_call(ws, ws_bytes, stream);
   const long long width = static_cast<long long>(p.kv_heads) * kHeadDim;
   if ((st = read_stride(&k_stride, width, dt)) != MOVA_OK || (st = read_stride(&v_stride, width, dt)) != MOVA_OK)
     return st;
@@ -180,7 +191,7 @@ mova_status mova_page_bounds(const mova_pages* pages, const int32_t* table, long
   mova_status st = read_pages(pages, &p);
   if (st == MOVA_OK) st = read_table(p, table, table_stride, max_pages, lens, B, &a);
   if (st != MOVA_OK) return st;
-  if (B == 0) return MOVA_OK;
+  if (B == 0) return empty_call(ws, ws_bytes, stream);
   if (!p.k || !cached || !k_lo || !k_hi || !aligned(cached, 4) || !aligned(k_lo, 16) || !aligned(k_hi, 16))
     return MOVA_ERR_INVALID_ARG;
   if ((st = check_ws(ws, ws_bytes, kStatusBytes)) != MOVA_OK) return st;
@@ -200,7 +211,7 @@ mova_status mova_page_attend(const void* q, mova_dtype q_dt, long long q_stride,
   if (st != MOVA_OK) return st;
   if (!io_fits(q_dt, p.dtype)) return MOVA_ERR_UNSUPPORTED;
   if (picked == nullptr ? top != 0 : top < 1) return MOVA_ERR_INVALID_ARG;
-  if (B == 0) return MOVA_OK;
+  if (B == 0) return empty_call(ws, ws_bytes, stream);
   if ((st = read_stride(&q_stride, static_cast<long long>(H) * kHeadDim, q_dt)) != MOVA_OK) return st;
   if (!q || !o || !p.k || !p.v || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(picked, 4))
     return MOVA_ERR_INVALID_ARG;
@@ -222,7 +233,7 @@ mova_status mova_page_select(const void* q, mova_dtype q_dt, long long q_stride,
   if (st != MOVA_OK) return st;
   if (!io_fits(q_dt, p.dtype)) return MOVA_ERR_UNSUPPORTED;
   if (top < 1) return MOVA_ERR_INVALID_ARG;
-  if (B == 0) return MOVA_OK;
+  if (B == 0) return empty_call(ws, ws_bytes, stream);
   if ((st = read_stride(&q_stride, static_cast<long long>(H) * kHeadDim, q_dt)) != MOVA_OK) return st;
   if (!q || !k_lo || !k_hi || !picked || !aligned(q, 16) || !aligned(k_lo, 16) || !aligned(k_hi, 16) ||
       !aligned(picked, 4))

@@ -167,6 +167,13 @@ def test_select_refuses(lib, kw, want):
     assert _lib.STATUS_NAMES[call_select(lib, pages(k=0, v=0), **kw)] == "MOVA_ERR_" + want
 
 
+def test_empty_calls_refuse_a_workspace_that_cannot_hold_their_status(lib):
+    for ws in (dict(ws=FAKE + 16), dict(ws_bytes=255)):
+        assert _lib.STATUS_NAMES[call_write(lib, pages(), T=0, **ws)] == "MOVA_ERR_INVALID_ARG"
+        for call in (call_bounds, call_attend, call_select):
+            assert _lib.STATUS_NAMES[call(lib, pages(), B=0, **ws)] == "MOVA_ERR_INVALID_ARG"
+
+
 # ---- The binding ----------------------------------------------------------------
 
 def test_row_stride():

@@ -694,6 +694,33 @@ def test_select_more_heads_than_warps(api, dtype):
     check_select(api, (q, lo, hi, table, lens), 3)
 
 
+def test_empty_calls_report_themselves(api):
+    """A call of no tokens or requests leaves its own status, not the one before's:
+    in a workspace that has just been made, too, and when a graph replays it."""
+    s, e = P.make("bf16", [20, 70], 2, 4, 16), P.make("bf16", [], 2, 4, 16, width=3)
+    assert e["q"].shape[0] == e["table"].shape[0] == 0
+    lo, hi = bounds_of(s, 16)
+    k = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device="cuda")
+    none = ints([])
+    for empty in (lambda ws: api.page_write(k[:0], k[:0], none, s["k"], s["v"], ws=ws),
+                  lambda ws: api.page_bounds(s["k"], e["table"], none, none, lo, hi, ws=ws),
+                  lambda ws: api.page_select(e["q"], lo, hi, e["table"], none, 16, 3, ws=ws),
+                  lambda ws: api.page_attend(e["q"], s["k"], s["v"], e["table"], none, ws=ws)):
+        api.page_write(k, k, ints([-7]), s["k"], s["v"])
+        ok(api, ("MOVA_ERR_DEVICE_CHECK", 0))
+        empty(None)
+        ok(api)
+        ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+        empty(ws)
+        assert api.get_status(ws) == ("MOVA_OK", 0)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            empty(ws)
+        ws.fill_(255)
+        graph.replay()
+        assert api.get_status(ws) == ("MOVA_OK", 0)
+
+
 # ---- Streams, graphs, repetition -----------------------------------------------------
 
 def test_repeated_calls_are_bit_identical(api):
