@@ -31,7 +31,7 @@ import torch
 from . import _lib
 
 _DT = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float16: _lib.F16,
-       torch.int32: _lib.I32, torch.int8: _lib.I8, torch.float8_e4m3fn: _lib.E4M3}
+       torch.int32: _lib.I32, torch.int8: _lib.I8}
 _PATH = {"auto": _lib.PATH_AUTO, "stream": _lib.PATH_STREAM, "tensor": _lib.PATH_TENSOR,
          "tensor_1cta": _lib.PATH_TENSOR_1CTA}
 
@@ -483,6 +483,7 @@ def value_attend_host(x: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, Wv: t
 # fused projection's output.  Types: fp32 with fp32 caches; bf16 with bf16 or
 # float8_e4m3fn caches, the latter with one fp32 scale per KV head.
 
+_CACHE_DT = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16, torch.float8_e4m3fn: _lib.E4M3}
 _CACHE_IO = {torch.float32: torch.float32, torch.bfloat16: torch.bfloat16, torch.float8_e4m3fn: torch.bfloat16}
 _STATUS_BYTES = 256
 _I32 = torch.int32
@@ -574,7 +575,7 @@ def _pages(index: int, k_cache, v_cache=None, k_scale=None, v_scale=None):
         vs = 0 if v_scale is None else _vector(v_scale, "v_scale", kv, index, torch.float32)
     if k_cache.get_device() != index:
         _on(index, k_cache=k_cache)
-    return _PAGES.pack(k_cache.data_ptr(), v, _DT[dtype], num, kv, page, k_stride, v_stride, ks, vs), num, kv
+    return _PAGES.pack(k_cache.data_ptr(), v, _CACHE_DT[dtype], num, kv, page, k_stride, v_stride, ks, vs), num, kv
 
 
 def _table(index: int, table, B: int):
@@ -723,7 +724,7 @@ def page_select(q: torch.Tensor, k_lo: torch.Tensor, k_hi: torch.Tensor, table: 
     p_table, stride, max_pages = _table(index, table, B)
     p_lens = _vector(lens, "lens", B, index)
     picked = torch.empty(B, kv, top, dtype=_I32, device=dev)
-    p = _PAGES.pack(0, 0, _DT[dtype], num, kv, page_size, 0, 0, 0, 0)
+    p = _PAGES.pack(0, 0, _CACHE_DT[dtype], num, kv, page_size, 0, 0, 0, 0)
     p_ws, n_ws, stream = _page_ws(ws, page_workspace_size(B, max_pages, kv, H), dev)
     code = _lib.load().mova_page_select(q.data_ptr(), _DT[q.dtype], q_stride, H, p, k_lo.data_ptr(), k_hi.data_ptr(),
                                         p_table, stride, max_pages, p_lens, B, top, picked.data_ptr(), p_ws, n_ws, stream)

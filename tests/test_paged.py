@@ -297,6 +297,13 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
     assert seen == [s["q"].device, "out"]
 
 
+def test_the_value_path_knows_no_8_bit_floats(lib):
+    """E4M3 is a type of cache pages alone."""
+    assert api.auto_path(100, torch.bfloat16) == "tensor"
+    with pytest.raises(KeyError):
+        api.auto_path(100, torch.float8_e4m3fn)
+
+
 def test_packed_pages_are_the_struct():
     p = _lib.Pages(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
     assert bytes(p) == api._PAGES.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10)
