@@ -613,7 +613,7 @@ template <int M> __device__ __forceinline__ void store_out(void* o, long long at
 }
 
 // What a cluster's CTAs share at the end: unnormalised outputs, then maxima and sums.
-constexpr int kMineFloats = kMaxGroup * kPartRow;
+template <int M, int NT> constexpr int kMineFloats = (M == kF32 ? NT : 8 * NT) * kPartRow;
 
 // The status of a call without a second kernel, by one cluster of its own: every
 // length, and every table entry that the other clusters look up.
@@ -1186,6 +1186,10 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
         log_sum<M>(m, l));
 }
 
+// Shared memory of an SM to count on, and what a CTA takes of it beyond the dynamic: at
+// most 1 KB of static memory, and 1 KB that the system keeps.
+constexpr size_t kSmShared = 227 << 10, kCtaReserve = 2048;
+
 // Rows from which warps work alone.  Measured on bf16: 8192 rows of 100 tokens
 // 135 us alone, 212 in teams; 512 rows of 4096 171 and 169; 64 rows to 500
 // 13.2 and 7.7.
@@ -1197,6 +1201,25 @@ long long row_tokens(const AttendArgs& s) {
   return pages << s.a.shift;
 }
 
+// A launch of clusters of `size` CTAs.
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  ClusterLaunch(long long clusters, int size, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * size));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
 template <int M, int NT, int kTeam>
 cudaError_t launch_clusters(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, long long clusters, int size,
                             size_t smem) {
@@ -1204,25 +1227,37 @@ cudaError_t launch_clusters(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   static bool done[64] = {false};
   cudaError_t err = prepare_kernel(kern, smem, done);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(clusters * size));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = size;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  const ClusterLaunch launch(clusters, size, smem, stream);
   note_launch();
-  return cudaLaunchKernelEx(&cfg, kern, s, sb);
+  return cudaLaunchKernelEx(&launch.cfg, kern, s, sb);
+}
+
+// Clusters of 2^i CTAs that are resident at once: fewer than the SMs' CTAs make, as a
+// cluster lies in one group of SMs.  Asked for once per device.
+template <int M, int NT>
+int resident_clusters(int i, size_t smem) {
+  static int known[64][4] = {};  // and one more; 0: not asked yet
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  if (known[dev][i] == 0) {
+    auto kern = page_attend_kernel<M, NT, kWarps, true>;
+    static bool done[64] = {false};
+    ClusterLaunch launch(1, 1 << i, smem, nullptr);
+    launch.cfg.numAttrs = 1;
+    int n = 0;
+    if (prepare_kernel(kern, smem, done) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &launch.cfg) != cudaSuccess) {
+      cudaGetLastError();  // not the next caller's
+      return 0;
+    }
+    known[dev][i] = n + 1;
+  }
+  return known[dev][i] - 1;
 }
 
 // One launch, a cluster to a row: for calls that have few rows, all of whose
-// clusters are resident, and whose rows cannot be long.  It saves the second
+// clusters are resident (35 bf16 rows of 1000 tokens: 7.4 us in clusters of 4, 10.6
+// in clusters of 8, of which 33 are), and whose rows cannot be long.  It saves the second
 // launch and the partial results' way through memory, about 2.5 us and as much
 // of the host's time, and loses where lengths differ, as one cluster may then
 // have what all would share.  So a CTA has at most kOwnBytes, which it reads in
@@ -1239,16 +1274,16 @@ constexpr long long kOwnBytes = 256 << 10;
 template <int M, int NT>
 bool launch_own(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, cudaError_t* err) {
   constexpr int kUnit = kWarps * Tile<M>::keys, kKeyBytes = 2 * kHeadDim * sizeof(typename Tile<M>::E);
-  constexpr size_t kSmem = attend_smem<M, NT, kWarps>(0) + kMineFloats * 4;
+  constexpr size_t kSmem = attend_smem<M, NT, kWarps>(0) + kMineFloats<M, NT> * 4;
+  static_assert(ctas_per_sm<M, NT>() * (kSmem + kCtaReserve) <= kSmShared, "as many CTAs as are counted on an SM");
   const long long rows = static_cast<long long>(s.a.B) * s.a.kv, units = (row_tokens(s) + kUnit - 1) / kUnit;
-  const long long resident = static_cast<long long>(sm_count()) * ctas_per_sm<M, NT>();
   int size = 1;
-  while (size < kMaxCluster && (rows + 1) * size * 2 <= resident && size < units) size *= 2;
+  for (int i = 1; i < 4 && size < units && rows < resident_clusters<M, NT>(i, kSmem); ++i) size *= 2;
   const long long own = kIsF32<M> ? (rows * size < sm_count() ? kOwnBytes / 2 : kOwnBytes)
                                   : (s.picked != nullptr ? 2 * kOwnBytes : kOwnBytes);
   // What one cluster checks for the status, 32 table entries a thread at most.
   const long long entries = s.picked == nullptr ? static_cast<long long>(s.a.B) * s.a.max_pages : rows * s.top;
-  if ((rows + 1) * size > resident || (units + size - 1) / size * kUnit * kKeyBytes > own ||
+  if ((size == 1 && rows >= resident_clusters<M, NT>(0, kSmem)) || (units + size - 1) / size * kUnit * kKeyBytes > own ||
       entries > size * kThreads * 32)
     return false;
   *err = launch_clusters<M, NT, kWarps>(s, sb, stream, rows + 1, size, kSmem);
@@ -1286,7 +1321,7 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   if (err != cudaSuccess) return err;
   const size_t smem = attend_smem<M, NT, kTeam>(s.a.B);
   // All CTAs are resident at once, as each takes an equal share.
-  const int per_sm = std::max(1, std::min(ctas_per_sm<M, NT>(), static_cast<int>((227 * 1024) / (smem + 2048))));
+  const int per_sm = std::max(1, std::min(ctas_per_sm<M, NT>(), static_cast<int>(kSmShared / (smem + kCtaReserve))));
   constexpr int kCta = kWarps * kLeast<M, kTeam> * Tile<M>::keys;  // tokens that keep a CTA busy
   const long long most = static_cast<long long>(s.a.B) * s.a.kv * ((row_tokens(s) + kCta - 1) / kCta);
   const int ctas = static_cast<int>(std::max(1LL, std::min({static_cast<long long>(sm_count()) * per_sm, most,

@@ -339,6 +339,23 @@ def test_attend_uneven_rows_of_a_wide_table(api, dtype, G, seed):
     check_attend(api, P.make(dtype, lens, 3 + seed, G, 32, seed=seed, width=1500), dtype)
 
 
+@pytest.mark.parametrize("dtype,G", [("f32", 4), ("f32", 8), ("bf16", 4), ("bf16", 16), ("e4m3", 8), ("e4m3", 16)])
+@pytest.mark.parametrize("rows", [16, 33, 36, 48, 51, 72, 105, 300, 440])
+def test_attend_rows_about_what_is_resident(api, dtype, G, rows):
+    lens = [(61 * i) % 203 for i in range(rows)]
+    check_attend(api, P.make(dtype, lens, 1, G, 16, seed=rows, width=13), dtype)
+
+
+def test_attend_takes_clusters_that_are_all_resident(api):
+    """36 rows and the status in clusters of 8, two CTAs an SM, would have to fill 148
+    SMs without a gap, but clusters lie in groups of SMs: two launches."""
+    for rows, launches in ((8, 1), (36, 2)):
+        s = P.make("bf16", [100] * rows, 1, 4, 32, width=125)
+        before = api.launch_count()
+        check_attend(api, s, "bf16")
+        assert api.launch_count() - before == launches
+
+
 def test_attend_many_requests(api):
     lens = [(7 * i) % 23 for i in range(4096)]
     check_attend(api, P.make("bf16", lens, 1, 2, 16), "bf16")
