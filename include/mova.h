@@ -554,8 +554,11 @@ mova_status mova_page_bounds(const mova_pages* pages, const int32_t* table, long
  * With E4M3 pages a weight p_i enters the sum over v_i rounded to 2^-11 of
  * itself, or to 2^-40 of the greatest, whichever is more.
  * NaN and infinite keys or values that count show in o as the formula has it,
- * except that with fp32 pages and more than 4 query heads to a KV head an
- * infinite one shows as NaN. */
+ * except that
+ *  - a row all of whose scores are -inf counts as one without tokens;
+ *  - an infinite value whose weight is below 2^-100 of the row's greatest may
+ *    show as NaN, and with fp32 pages and more than 4 query heads to a KV head
+ *    any infinite key or value does. */
 mova_status mova_page_attend(const void* q, mova_dtype q_dt, long long q_stride, int H, const mova_pages* pages,
                              const int32_t* table, long long table_stride, int max_pages, const int32_t* lens, int B,
                              float scale, const int32_t* picked, int top, void* o, float* lse, void* ws,

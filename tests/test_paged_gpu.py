@@ -462,6 +462,46 @@ def test_attend_nan_and_infinities_show(api, dtype):
     assert not torch.isfinite(o[2, :2]).any() and torch.isfinite(o[2, 2:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("width", [None, 3000])
+@pytest.mark.parametrize("rows", [4, 1100])
+def test_attend_scores_of_minus_infinity(api, dtype, width, rows):
+    """A token whose score is -inf has no weight; a row of such tokens counts as one
+    without tokens."""
+    s = P.make(dtype, [1, 17, 40, 33] * (rows // 4), 1, 3, 16, seed=5, width=width, fused=False)
+    s["q"] = s["q"].abs() + 0.5
+    want = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], return_lse=True)
+    for b in range(0, rows, 4):
+        s["k"][s["table"][b, 0].item(), 0, 0, 7] = -math.inf
+        s["k"][s["table"][b + 1, :2].long(), :, :, 9] = -math.inf
+    s["k"][s["table"][2, 2].item(), 0, :8, 0] = -math.inf  # the last eight of 40
+    o, lse = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], return_lse=True)
+    ok(api)
+    for b in (0, 1, rows - 4, rows - 3):
+        assert (o[b] == 0).all() and (lse[b] == -math.inf).all()
+    assert torch.equal(o[3], want[0][3]) and torch.equal(lse[3], want[1][3])
+    s["lens"][2] = 32
+    few = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], return_lse=True)
+    # The same sums of 32 terms, in another order: 2 * 32 u of them, with |v| below 6, and both outputs' rounding.
+    assert ((o[2] - few[0][2]).abs() <= 2 * P.OUT[dtype] * few[0][2].abs() + 2 * 2 * 32 * P.U * 6).all()
+    assert ((lse[2] - few[1][2]).abs() <= 2 * 2 * 32 * P.U + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [5, 300])
+def test_attend_infinite_value_of_little_weight(api, dtype, n):
+    """A weight of 2^-90 of the greatest, and an infinite value: as in the formula."""
+    s = P.make(dtype, [n], 1, 2, 16, seed=5, fused=False)
+    s["q"] = torch.ones_like(s["q"])
+    s["k"].zero_()
+    s["v"].fill_(1.0)
+    s["k"][s["table"][0, 0].item(), 0, 0, 0] = 90.0
+    s["v"][s["table"][0, (n - 1) // 16].item(), 0, (n - 1) % 16, 3] = -math.inf
+    o = api.page_attend(s["q"], s["k"], s["v"], s["table"], s["lens"], scale=math.log(2.0))
+    ok(api)
+    assert (o[..., 3] == -math.inf).all() and torch.isfinite(o[..., :3]).all() and torch.isfinite(o[..., 4:]).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
 def test_attend_bad_pages_count_as_absent(api, dtype):
     s = P.make(dtype, [100, 64, 48], 2, 4, 16, seed=6)
