@@ -15,9 +15,11 @@ Every function enqueues on torch's current CUDA stream (the host-buffer forms:
 on `stream` if given) and returns without synchronising.  Device-side checks
 are read with get_status().  A call given no `ws` uses the workspace this
 module keeps for its device and stream, so calls on different streams may
-overlap on the GPU.  Calls that share a `ws` must run on one stream.  A paged
-call that a graph captures without a `ws` has one in the graph's own memory,
-whose status get_status() does not read: give it a `ws` to read one.
+overlap on the GPU.  Calls that share a `ws` must run on one stream.  A value
+call that a graph captures without a `ws` has the capturing stream's, so that
+such graphs are replayed on that stream.  A paged call that a graph captures
+without a `ws` has one in the graph's own memory, whose status get_status() does
+not read: give it a `ws` to read one.
 """
 from __future__ import annotations
 
@@ -92,15 +94,28 @@ def _shape(t: torch.Tensor, name: str, want) -> None:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(want)}")
 
 
+def _under_capture(dev: torch.device) -> bool:
+    return dev.type == "cuda" and _capturing()
+
+
 class Workspace:
-    """A device workspace that grows on demand."""
+    """A device workspace that grows on demand.  A buffer that a call under
+    stream capture was given is in that call's graph: it is kept when a larger
+    one takes its place."""
 
     def __init__(self):
         self.buf: Optional[torch.Tensor] = None
+        self.in_graph = False
+        self.kept = []
 
     def get(self, nbytes: int, device) -> torch.Tensor:
-        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != torch.device(device):
-            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        dev = torch.device(device)
+        if self.buf is None or self.buf.numel() < nbytes or self.buf.device != dev:
+            if self.in_graph:
+                self.kept.append(self.buf)
+            self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+            self.in_graph = False
+        self.in_graph = self.in_graph or _under_capture(dev)
         return self.buf
 
 
@@ -140,7 +155,8 @@ def release_workspaces() -> None:
     """Drop the default workspaces (each stream that ran a call without `ws`
     keeps one, sized for its largest call, until this is called).  Safe with
     calls still in flight: torch's caching allocator reuses a freed buffer
-    only for later work on the stream that used it."""
+    only for later work on the stream that used it.  Not while a graph that
+    holds a value call made without `ws` is to be replayed."""
     _WS.clear()
 
 

@@ -4,6 +4,7 @@ each (device, stream) gets its own workspace; calls on one stream share it,
 and it is allocated with its stream current, so that torch's caching
 allocator ties the memory to the stream that uses it."""
 import contextlib
+import weakref
 
 import pytest
 import torch
@@ -132,3 +133,18 @@ def test_value_refuses_mismatched_shapes(monkeypatch, case):
         Wv = _Tensor(E, n, d + 64)
     with pytest.raises(ValueError, match="shape"):
         api.value(x, idx, w, Wv)
+
+
+def test_a_workspace_that_a_graph_uses_outlives_its_replacement(fresh, monkeypatch):
+    """A value call that a graph captures has the stream's workspace in the graph:
+    a later, larger call gets another, but the first is not given back."""
+    capturing = [True]
+    monkeypatch.setattr(api, "_under_capture", lambda dev: capturing[0], raising=False)
+    kept = weakref.ref(api._workspace(1000, "cpu"))
+    capturing[0] = False
+    big = weakref.ref(api._workspace(5000, "cpu"))  # no graph has this one
+    assert kept() is not None
+    api._workspace(9000, "cpu")
+    assert kept() is not None and big() is None
+    api.release_workspaces()
+    assert kept() is None

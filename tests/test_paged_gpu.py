@@ -912,6 +912,32 @@ def test_captured_calls_have_their_own_workspaces(api):
     assert (filler == 255).all()
 
 
+def test_captured_value_call_keeps_its_workspace(api):
+    """value_routed in a graph, after a call that needed a larger workspace on the
+    capturing stream and work that takes whatever memory is free."""
+    d, E, n = 256, 8, 256
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rnd = lambda *shape: torch.randn(*shape, generator=g, device="cuda")
+    x, Wr, br, Wv = rnd(40, d).bfloat16(), 0.1 * rnd(E, d), 0.01 * rnd(E), (rnd(E, n, d) / 16).bfloat16()
+    want = api.value_routed(x, Wr, br, Wv, 2)
+    big = P.make("bf16", [40] * 64, 8, 16, 16, seed=5)
+    assert api.page_workspace_size(64, 3, 8, 128) > api.workspace_size(40, d, E, 2, n)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        api.value_routed(x, Wr, br, Wv, 2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        v = api.value_routed(x, Wr, br, Wv, 2)
+    with torch.cuda.stream(side):
+        api.page_attend(big["q"], big["k"], big["v"], big["table"], big["lens"])
+        filler = [torch.full((1 << k,), 255, dtype=torch.uint8, device="cuda") for k in range(12, 22) for _ in range(8)]
+        for _ in range(3):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(v, want) and all((f == 255).all() for f in filler)
+
+
 # ---- With the value path ----------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "e4m3"])
