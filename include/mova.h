@@ -509,7 +509,9 @@ size_t mova_page_workspace_size(int B, int max_pages, int kv_heads, int H);
  * last one: it takes no page, lens[b] = cached[b] (0 if negative), its tokens
  * get slot and position -1.  A token whose page number lies outside
  * [0, num_pages) gets slot -1; tokens past T get none.  The status tells the
- * first request that any of these befell.  `taken` outside [0, n_free] counts
+ * first request that any of these befell.  T is to be at least the sum of
+ * added: lens counts tokens past it all the same, and where they would lie a
+ * reader of lens finds what the pages held before.  `taken` outside [0, n_free] counts
  * as no page left.  No output may overlap an input, taken_out apart. */
 mova_status mova_page_map(const int32_t* cached, const int32_t* added, int B, int32_t* table, long long table_stride,
                           int max_pages, const int32_t* free_pages, int n_free, const int32_t* taken, int page_size,
@@ -575,10 +577,12 @@ mova_status mova_page_attend(const void* q, mova_dtype q_dt, long long q_stride,
  * A NaN score counts as the greatest.  Scores are of the stored values
  * (E4M3: without the head's scale, which changes no order).  q as in
  * mova_page_attend; of `pages` only dtype, num_pages, kv_heads and page_size
- * are read.  picked (B, kv_heads, top) int32 out.  Where some score of a row
- * is not finite or its products may sum to more than 2^126, or hundreds lie
- * within rounding of the last one taken, bf16 and E4M3 pages take longer: all
- * of the row's pages are scored in fp64. */
+ * are read.  picked (B, kv_heads, top) int32 out.  bf16 and E4M3 pages are
+ * scored in fp32 first.  Where some score of a row is not finite or its
+ * products may sum to more than 2^126, or where hundreds of scores lie closer
+ * to the last one taken than 2^-12 of sum |q_d| times the row's greatest bound
+ * -- many pages alike, or one with bounds hundreds of times the others' -- all
+ * of the row's pages are scored in fp64, which takes up to 30 times as long. */
 mova_status mova_page_select(const void* q, mova_dtype q_dt, long long q_stride, int H, const mova_pages* pages,
                              const void* k_lo, const void* k_hi, const int32_t* table, long long table_stride,
                              int max_pages, const int32_t* lens, int B, int top, int32_t* picked, void* ws,

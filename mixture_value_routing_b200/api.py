@@ -640,7 +640,8 @@ def page_map(cached: torch.Tensor, added: torch.Tensor, table: torch.Tensor, fre
     all int32.  Writes the new pages into `table`; `taken` counts the entries
     of free_pages handed out so far, and the new count goes to taken_out
     (which may be `taken` itself) or to a new tensor.  `tokens` is the size of
-    the step's token batch; slots and positions past the last token are -1."""
+    the step's token batch, at least the sum of `added`; slots and positions past
+    the last token are -1."""
     if _elsewhere(cached):
         with torch.cuda.device(cached.device):
             return page_map(cached, added, table, free_pages, taken, page_size, num_pages, tokens, taken_out, ws)

@@ -1190,9 +1190,11 @@ page_join_kernel(const AttendArgs s, int ctas, StatusBlock* sb) {
 // most 1 KB of static memory, and 1 KB that the system keeps.
 constexpr size_t kSmShared = 227 << 10, kCtaReserve = 2048;
 
-// Rows from which warps work alone.  Measured on bf16: 8192 rows of 100 tokens
-// 135 us alone, 212 in teams; 512 rows of 4096 171 and 169; 64 rows to 500
-// 13.2 and 7.7.
+// Rows from which warps work alone.  Measured alone and in teams, where the table
+// could hold 131072 tokens a request: bf16, 2048 rows of 100 tokens 28.1 and 32.7
+// us, 8192 (4096 requests) 140 and 203, 1024 of up to 1000 45.3 and 45.5, of 500 50.7
+// and 47.4; 512 of 500 30.1 and 28.2, of 4096 170 and 165; E4M3, 1024 of up to 1000
+// 28.8 and 30.4; fp32 83 and 80.
 constexpr int kAloneRows = 1024;
 
 // Tokens of a row that may be attended, by the host's knowledge.
@@ -1260,14 +1262,17 @@ int resident_clusters(int i, size_t smem) {
 // in clusters of 8, of which 33 are), and whose rows cannot be long.  It saves the second
 // launch and the partial results' way through memory, about 2.5 us and as much
 // of the host's time, and loses where lengths differ, as one cluster may then
-// have what all would share.  So a CTA has at most kOwnBytes, which it reads in
-// about 4 us; twice that of picked pages, of which every long row has the same
-// number; but of fp32 pages, whose products take longer, not that, and half
-// where the clusters leave SMs free.
+// have what all would share.  So a CTA has at most kOwnBytes, which a full grid, two
+// CTAs an SM, reads in 12 us; twice that of picked pages, of which every long row
+// has the same number; but of fp32 pages, whose products take longer, not that, and
+// half where the clusters leave SMs free.
 // Measured, one launch and two: bf16, 8 KV heads, 8 requests of 250 tokens 5.6
 // and 8.6 us, 8 of 2000 14.9 and 18.8, 1 of 4000 8.8 and 10.3, 1 of 8000 13.0
 // and 12.2; fp32, 4 of 2000 16.7 and 19.4, 1 of 2000 with one KV head 10.7 and
-// 7.4, 5 to 3001 with 7 heads a KV head 18 and 14.  Clusters of 16 gained 0.7 us
+// 7.4, 5 to 3001 with 7 heads a KV head 18 and 14.  Picked pages of 64, bf16: 8 rows
+// of 64 pages 9.0 and 9.6, 32 of 64 15.1 and 19.8, 32 of 96 20.0 and 24.7, 16 of 128
+// (kOwnBytes twice) 16.9 and 18.4; E4M3: 8 of 64 7.8 and 9.4, 16 of 128 14.0 and
+// 15.8, but 16 of 256 (twice) 22.1 and 20.3; fp32, 8 of 16 7.5 and 9.3.  Clusters of 16 gained 0.7 us
 // for one request of 4000 and lost 0.8 for one of 500.  False: the call is not
 // one for it.
 constexpr long long kOwnBytes = 256 << 10;
@@ -1293,13 +1298,15 @@ bool launch_own(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, cudaE
 // One launch, a warp to a row: where clusters would not all be resident and rows
 // cannot be long.  CTAs come and go, so that many short rows need no scan of the
 // lengths (whose place in shared memory leaves one CTA an SM for 4096 requests),
-// no partial results and no second kernel.  A row may have kWarpBytes, which a
-// warp reads in about 8 us; twice that of 1024 rows or more, where the last rows
-// are a small part of the time, but not of fp32, whose rows take longer.
-// Measured, one launch and two: bf16 8192 rows of 100 tokens 87 and 137 us, of
-// 20 43 and 71; 512 of 200 14.7 and 17.3; 1024 of 400 37 and 42; 640 to 500 26
-// and 23; E4M3 1024 of 200 13 and 19, 2048 of 400 50 and 47; fp32 8192 of 100
-// 164 and 173, 2048 of 200 98 and 78.  False: the call is not one for it.
+// no partial results and no second kernel.  A row may have kWarpBytes, which the
+// warps of a full grid, eight an SM, read in 24 us; twice that of 1024 rows or more,
+// where the last rows are a small part of the time, but not of fp32, whose rows
+// take longer.  Measured, one launch and two: bf16 8192 rows of 100 tokens 82 and
+// 140 us as 4096 requests, 80 and 86 as 1024; of 20 43 and 71; 512 of 200 14.7 and
+// 17.7; 1024 of 400 37 and 42; 640 to 500 26 and 22; E4M3 1024 of 200 14 and 19, of
+// 400 23 and 27, 4096 of 400 76 and 80, but 2048, a few more than the 1776 warps that
+// run at once, of 300 40 and 37, of 400 49 and 45; fp32 8192 of 100 162 and 162, 2048
+// of 200 98 and 78.  False: the call is not one for it.
 constexpr long long kWarpBytes = 128 << 10;
 template <int M, int NT>
 bool launch_warps(const AttendArgs& s, StatusBlock* sb, cudaStream_t stream, cudaError_t* err) {
@@ -1320,7 +1327,11 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   cudaError_t err = prepare_kernel(kern, attend_smem<M, NT, kTeam>(kMaxRequests), done);
   if (err != cudaSuccess) return err;
   const size_t smem = attend_smem<M, NT, kTeam>(s.a.B);
-  // All CTAs are resident at once, as each takes an equal share.
+  // All CTAs are resident at once, as each takes an equal share.  The prefix of many
+  // requests takes the place of rings: bf16 has one CTA an SM from 3904 requests on (3800
+  // of 100 tokens 60 us, 4000 83; of 500 177 for 3800, 232 for 4096), E4M3 two from 2410
+  // on (2300 of 500 68 us, 2500 80), fp32 with up to 4 heads two from 363 on where warps
+  // work alone.
   const int per_sm = std::max(1, std::min(ctas_per_sm<M, NT>(), static_cast<int>(kSmShared / (smem + kCtaReserve))));
   constexpr int kCta = kWarps * kLeast<M, kTeam> * Tile<M>::keys;  // tokens that keep a CTA busy
   const long long most = static_cast<long long>(s.a.B) * s.a.kv * ((row_tokens(s) + kCta - 1) / kCta);
@@ -1329,9 +1340,9 @@ cudaError_t launch_attend_t(const AttendArgs& s, StatusBlock* sb, cudaStream_t s
   err = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, s, sb);
   if (err != cudaSuccess) return err;
   // Few rows have many parts each, and leave SMs free: a CTA per head, of four
-  // warps, or of sixteen from 8 parts a row on.  Measured, 16 and 4 warps: one row
-  // of 65536 tokens with 16 heads, 296 parts, 18.5 and 23.1 us; 16 rows, 18 parts,
-  // 87.3 and 88.3.
+  // warps, or of sixteen from 8 parts a row on.  Measured, 16, 4 and 1 warps: one row
+  // of 65536 tokens with 16 heads, 296 parts, 20.3, 25.5 and 55.6 us; 16 rows of 32768
+  // with 4, 18 parts, 48.2, 48.8 and 50.0; 32 of 20000, 9 parts, 57.3, 56.2 and 57.3.
   const int rows = s.a.B * s.a.kv;
   if (static_cast<long long>(rows) * s.G <= 4LL * sm_count()) {
     if (ctas * (kWarps / kTeam) >= 8 * rows) {

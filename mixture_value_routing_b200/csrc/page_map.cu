@@ -7,7 +7,11 @@
 //               pos = cached[b] + i - starts[b], b the request of token i
 //
 // 8 bytes per request in, 8 bytes per new token out: latency bounds it, so it
-// is one launch, of one cluster of up to 8 CTAs.  Every CTA scans all
+// is one launch, of one cluster of up to 8 CTAs.  Measured: 64 requests of a token
+// each 3.2 us; 256 requests and 46590 new tokens 11.2, as a thread searches the
+// requests of five or six tokens one after another; 4096 requests and 15210 tokens
+// 22.7, as the scan and the checks go through the requests in four steps and a search
+// takes twelve.  Every CTA scans all
 // requests (at most 4096, in shared memory) and takes its share of the new
 // pages and tokens, finding a token's request by binary search.  A token in a
 // new page reads the free list, not the table, so no CTA waits for another's

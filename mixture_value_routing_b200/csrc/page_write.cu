@@ -4,15 +4,19 @@
 // alike), converted to the pages' type; E4M3 as round(k / scale), the quotient
 // formed in fp32 (IEEE division) and clamped to +-448.  Each element is read
 // and written once: a copy, bound by memory (16384 tokens of 8 bf16 heads, 134
-// MB: 22.7 us, 5.9 TB/s; loads and stores marked as streams, 25.2 us without
-// and with smaller CTAs).  A warp takes one token's keys or
+// MB: 22.8 us, 5.9 TB/s; loads and stores marked as streams, 25.2 us without
+// and with smaller CTAs; fp32, 269 MB: 43.3 us, 6.2 TB/s).  E4M3, 101 MB, takes 23.5
+// us, 4.3 TB/s: at 64 registers a thread to the others' 32 it has half as many warps
+// an SM.  A warp takes one token's keys or
 // values -- kv_heads * 128 elements, contiguous on the input side and 128 at a
 // time in the cache -- with 16-byte loads that do not wait for the slot.
 //
 // page_bounds: lo / hi[page, h, d] = min / max over the page's keys, for pages
 // that the step filled: page_size * 128 elements read for 256 written, bound
-// by memory.  Four warps share a (page, head), 16 keys each in flight at once, in
-// packed 16-bit minima and maxima, and join in shared memory, one barrier a page.
+// by memory.  Four warps share a (page, head), 16 keys each (E4M3: 64) in flight at
+// once, in packed 16-bit minima and maxima, and join in shared memory, one barrier a
+// page.  737 pages of 64 keys, 8 heads: fp32, 199 MB, 33.5 us, bf16 18.4, E4M3, 50
+// MB, 13.3; the first 4 us are the scan of the requests, the table and the first keys.
 #include <math.h>
 
 #include "paged.cuh"
@@ -168,8 +172,9 @@ cudaError_t launch_write_t(const void* k, const void* v, long long k_stride, lon
                     p.v_scale, p.kv_heads, shift, p.num_pages << shift, lanes, sb);
 }
 
-// Measured for 16384 tokens of 8 heads, bf16: 23.5 us with 512 threads, 25.2
-// with 256, 27.1 with 1024 (plain stores); for 64 tokens 2.3, 1.9 and 3.1.
+// Measured for 16384 tokens of 8 heads, bf16, before stores were marked as streams:
+// 23.5 us with 512 threads, 25.2 with 256, 27.1 with 1024; for 64 tokens 2.3, 1.9
+// and 3.1.
 template <typename In, typename Out, typename... Args>
 cudaError_t launch_write(int T, Args... args) {
   return T < kWriteSmall ? launch_write_t<In, Out, 256>(args...) : launch_write_t<In, Out, 512>(args...);
