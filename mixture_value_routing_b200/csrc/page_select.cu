@@ -1020,7 +1020,8 @@ cudaError_t launch_screened(const SelectArgs& s, StatusBlock* sb, cudaStream_t s
   return launch_pair(page_screen_kernel<E, NT>, page_pick_kernel<E, kThreads>, kThreads, kStored, s, NT, sb, done[0],
                      done[1], stream);
 }
-// Twice the threads where a row may have more scores than 512 hold.
+// Twice the threads where a row may have more scores than 512 hold (at 64 registers a
+// thread, so the selection spills 16 to 32 bytes).
 template <int NT>
 cudaError_t launch_select(const SelectArgs& s, mova_dtype dt, StatusBlock* sb, cudaStream_t stream) {
   const bool few = s.a.max_pages <= 512 * kHeld;
